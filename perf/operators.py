@@ -232,11 +232,7 @@ def prepare(case, seed):
             flat = torch.empty(sc.numel(), dtype=torch.uint8, device=dev)
             at = _chunk_index(n, k // _block(case), dev).flatten()
             flat[at] = sc.flatten()
-            sc = flat
-            if off is not None:
-                flat = torch.empty(off.numel(), dtype=torch.bfloat16, device=dev)
-                flat[at] = off.flatten()
-                s["off"] = flat
+            sc = flat  # offsets stay row-major
         s["scales"] = sc.contiguous()
         return s
     d, kv, heads = case["dim"], case["kv"], case["heads"]
@@ -330,8 +326,7 @@ def run(s):
         n, nb = case["n"], case["k"] // _block(case)
         sc, off = s["scales"], s["off"]
         if case["chunked"]:
-            at = _chunk_index(n, nb, sc.device)
-            sc, off = sc[at], None if off is None else off[at]
+            sc = sc[_chunk_index(n, nb, sc.device)]
         w = _values(fmt, s["codes"], sc, s["ts"], off, torch.float32)
         return (s["x"].float() @ w.T).to(dt)
     d, kv, heads = case["dim"], case["kv"], case["heads"]
@@ -417,8 +412,7 @@ def exact(case, seed):
         sc, off = s["scales"], s["off"]
         if case["chunked"]:
             # chunk (i, j) holds rows 128 i + 32 a + r and scales 4 j + b at place 16 r + 4 a + b
-            undo = lambda t: t.view(n // 128, nb // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(n, nb)  # noqa: E731
-            sc, off = undo(sc), None if off is None else undo(off)
+            sc = sc.view(n // 128, nb // 4, 32, 4, 4).permute(0, 3, 2, 1, 4).reshape(n, nb)
         x = s["x"].double()
         part = [x @ decode(s["codes"][i:i + 8192], sc[i:i + 8192], s["ts"], None if off is None else off[i:i + 8192]).T
                 for i in range(0, n, 8192)]
