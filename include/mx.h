@@ -417,6 +417,34 @@ int mx_mbs_gemm_scales(const mx_config *cfg, const uint8_t *scales, const uint8_
                        void *workspace, int64_t workspace_bytes, void *stream);
 
 /*
+ * mx_gemv -- matrix-vector products on 4-bit block-scaled weights with the
+ * activations unquantized ([MXFP4-OAS] Sec.2 formats; the pages' GEMMs take
+ * quantized operands on both sides and 128 rows at least, this is the product
+ * of a decode step): y[M x N] = x[M x K] W^T, W = x_hat of mx_dequantize.
+ *   cfg          the configuration W (N x K) was quantized with: row axis, E2M1,
+ *                E3M0 or INT4 elements, any scale format, rule, block size and
+ *                scale layout, macro scales; offsets (asymmetric) with blocks of
+ *                32 and more; no rotation, no FP6 (MX_ERR_UNSUPPORTED).
+ *   x            device, bf16 or fp32 (x_dtype), row m at x + m ldx elements
+ *                (ldx >= K; any alignment of an element).
+ *   codes ... offsets   W as mx_quantize wrote it (offsets are row-major in both
+ *                scale layouts); tensor_scale is read unless cfg->tensor_scale
+ *                == MX_TS_NONE.
+ *   y            device, bf16 or fp32 (y_dtype), row m at y + m ldy elements
+ *                (ldy >= N); must not overlap an input.
+ * Products q x are exact and summed in binary32, one sum per block times its
+ * scale; every output is rounded once, and its value does not depend on
+ * timing.  x values of a 128-column chunk below 2^-31 of the chunk's largest
+ * are rounded at 2^-39 of it (binary32 x: at 2^-50).  An infinite or NaN x
+ * gives what IEEE sums of the products give; a NaN scale a NaN.
+ * 0 <= M <= 2^17; the weights are read once per 16 rows of bf16 x (8 of
+ * fp32).  No workspace; one launch.
+ */
+int mx_gemv(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t ldx, int64_t M, const void *codes,
+            const uint8_t *scales, const float *tensor_scale, const uint8_t *macro_scales, const uint16_t *offsets,
+            int64_t N, int64_t K, void *y, int32_t y_dtype, int64_t ldy, void *stream);
+
+/*
  * mx_tensor_peak -- tensor-core ceiling probe for the roofline of mx_gemm (the
  * pages have no counterpart; it measures the device, not the method).  One
  * CTA per SM issues `iters` stages of four 128 x 256 x K block-scaled MMAs of

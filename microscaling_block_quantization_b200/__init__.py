@@ -82,6 +82,14 @@ class Config:
                          self.axis, self.round, self.asymmetric, self.tensor_scale,
                          self.macro_block, self.hadamard, self.sf_layout, self.seed)
 
+    def ref(self):
+        """The C struct by reference, built once per instance."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = C.byref(self.c())
+            object.__setattr__(self, "_ref", r)
+        return r
+
 
 MXFP4 = Config()
 NVFP4 = Config(block=16, scale_fmt=SCALE_UE4M3, rule=RULE_NEAREST, tensor_scale=TS_COMPUTE)
@@ -119,6 +127,7 @@ def lib() -> C.CDLL:
         L.mx_gemm_workspace_bytes.restype = i64
         L.mx_gemm.argtypes = [cfgp, cfgp, P, P, P, P, P, P, i64, i64, i64, P, i32, P]
         L.mx_gemm_qsnr.argtypes = [cfgp, cfgp, P, P, i64, i64, i64, P, P, P, P, P, P, P, P, i64, P]
+        L.mx_gemv.argtypes = [cfgp, P, i32, i64, i64, P, P, P, P, P, i64, i64, P, i32, i64, P]
         L.mx_mbs_gemm_scales.argtypes = [cfgp, P, P, i64, i64, P, P, P, i64, P]
         L.mx_device_status.argtypes = [P, C.POINTER(i32)]
         L.mx_tensor_amax.argtypes = [cfgp, P, i32, i64, i64, P, i64, P]
@@ -130,7 +139,7 @@ def lib() -> C.CDLL:
         L.mx_version.restype = C.c_char_p
         for f in ("mx_query_sizes", "mx_quantize", "mx_quantize_group", "mx_quantize_noalloc",
                   "mx_hadamard_quantize", "mx_dequantize",
-                  "mx_qsnr", "mx_gemm", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
+                  "mx_qsnr", "mx_gemm", "mx_gemv", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
                   "mx_tensor_amax", "mx_stats_finalize", "mx_gemm_qsnr_finalize", "mx_tensor_peak"):
             getattr(L, f).restype = C.c_int
         _lib = L
@@ -246,6 +255,12 @@ def mx_gemm(ca: Config, cb: Config, Aq, Asf, Bq, Bsf, tsA, tsB, M, N, K, C_out, 
     a, b = ca.c(), cb.c()
     return lib().mx_gemm(C.byref(a), C.byref(b), Aq, Asf, Bq, Bsf, tsA, tsB, M, N, K, C_out,
                          c_dtype, stream)
+
+
+def mx_gemv(cfg: Config, x, x_dtype, ldx, M, codes, scales, tensor_scale, macro, offsets, N, K, y, y_dtype,
+            ldy, stream) -> int:
+    return lib().mx_gemv(cfg.ref(), x, x_dtype, ldx, M, codes, scales, tensor_scale, macro, offsets, N, K, y,
+                         y_dtype, ldy, stream)
 
 
 def mx_gemm_qsnr(ca: Config, cb: Config, A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB, stats,
@@ -479,6 +494,86 @@ def gemm(qa: Quantized, qb: Quantized, out_dtype: torch.dtype = torch.bfloat16,
                  _stream(stream))
     _check("mx_gemm", rc)
     return out
+
+
+# ---- decode-time operators --------------------------------------------------
+_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
+
+
+class _Launch:
+    """Device and stream of a call: the operands' device made current, and its
+    current stream (or the caller's ``stream``) both for the launch and for
+    what the call allocates."""
+
+    __slots__ = ("ctx",)
+
+    def __init__(self, device, stream):
+        self.ctx = []
+        if device.index != torch.cuda.current_device():
+            self.ctx.append(torch.cuda.device(device))
+        if stream is not None:
+            self.ctx.append(torch.cuda.stream(stream))
+
+    def __enter__(self):
+        for c in self.ctx:
+            c.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        for c in reversed(self.ctx):
+            c.__exit__(*e)
+
+
+def _same_device(device, **tensors) -> None:
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
+def _rows_of(t: torch.Tensor, name: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {t.dtype} of {name} (bf16 or fp32)")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    if t.shape[0] > 1:
+        if t.stride(0) < t.shape[1]:
+            raise ValueError(f"the rows of {name} overlap")
+        return t.stride(0)
+    return t.shape[1]
+
+
+def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *,
+         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """y = x W^T of a few rows x (``[M, K]`` or ``[K]``, bf16 or fp32, rows at
+    any stride) and 4-bit block-scaled weights W (``qw``, N x K, quantized along
+    K), activations unquantized (``mx_gemv``).  The result has x's dtype unless
+    ``out_dtype`` or ``out`` (``[M, N]``, rows at any stride) says otherwise.
+    On a ``stream`` of the caller's the result is allocated there; x and qw must
+    be ready on it."""
+    if not x.is_cuda:
+        raise ValueError("x must be a CUDA tensor")
+    if x.dim() not in (1, 2) or x.shape[-1] != qw.cols:
+        raise ValueError(f"x must be [M, {qw.cols}] or [{qw.cols}], got {list(x.shape)}")
+    x2 = x if x.dim() == 2 else x[None]
+    M, N, K = x2.shape[0], qw.rows, qw.cols
+    ldx = _rows_of(x2, "x")
+    dev = x.device
+    _same_device(dev, codes=qw.codes, scales=qw.scales, macro=qw.macro, offsets=qw.offsets, out=out,
+                 tensor_scale=qw.tensor_scale if qw.cfg.tensor_scale else None)
+    with _Launch(dev, stream) as st:
+        if out is None:
+            y = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
+        else:
+            if out.shape != x.shape[:-1] + (N,) or out.dtype != (out_dtype or out.dtype):
+                raise ValueError(f"out must be {list(x.shape[:-1]) + [N]} of {out_dtype or out.dtype}")
+            y = out if out.dim() == 2 else out[None]
+        ldy = _rows_of(y, "out")
+        rc = mx_gemv(qw.cfg, x2.data_ptr(), _DT[x.dtype], ldx, M, qw.codes.data_ptr(), qw.scales.data_ptr(),
+                     _ptr_or_none(qw.tensor_scale), _ptr_or_none(qw.macro), _ptr_or_none(qw.offsets), N, K,
+                     y.data_ptr(), _DT[y.dtype], ldy, st)
+    _check("mx_gemv", rc)
+    return out if out is not None else y if x.dim() == 2 else y[0]
 
 
 def mbs_gemm_operand(q: Quantized, stream=None) -> Quantized:

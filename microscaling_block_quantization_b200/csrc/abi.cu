@@ -8,6 +8,7 @@
 
 #include <new>
 
+#include "mma_decode.cuh"
 #include "mx.h"
 #include "mx_internal.h"
 
@@ -410,6 +411,60 @@ int mx_quantize_group(const mx_config *cfg, int32_t x_dtype, const mx_quantize_i
     delete[] ps;
     delete[] empty;
     return rc;
+}
+
+int mx_gemv(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t ldx, int64_t M, const void *codes,
+            const uint8_t *scales, const float *tensor_scale, const uint8_t *macro_scales, const uint16_t *offsets,
+            int64_t N, int64_t K, void *y, int32_t y_dtype, int64_t ldy, void *stream)
+{
+    if (!cfg) return MX_ERR_INVALID;
+    const int rc = check_config(cfg, N, K, cfg->hadamard != 0);
+    if (rc != MX_OK) return rc;
+    if (cfg->axis != MX_AXIS_ROW || cfg->hadamard || (cfg->asymmetric && cfg->block < 32) ||
+        cfg->elem == MX_E2M3 || cfg->elem == MX_E3M2)
+        return MX_ERR_UNSUPPORTED;
+    if (x_dtype != MX_DT_BF16 && x_dtype != MX_DT_FP32) return MX_ERR_INVALID;
+    if (y_dtype != MX_DT_BF16 && y_dtype != MX_DT_FP32) return MX_ERR_INVALID;
+    if (M < 0 || M > kMaxGemvRows) return MX_ERR_INVALID;
+    if (M == 0 || N == 0) return MX_OK;
+    if (ldx < K || ldy < N) return MX_ERR_INVALID;
+    if (!y) return MX_ERR_INVALID;
+    const int xs = x_dtype == MX_DT_FP32 ? 4 : 2, ys = y_dtype == MX_DT_FP32 ? 4 : 2;
+    if ((uintptr_t)y % ys) return MX_ERR_ALIGN;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (K == 0) return cuda_ok(cudaMemset2DAsync(y, ldy * ys, 0, N * ys, M, st));
+    if (!x || !codes || !scales) return MX_ERR_INVALID;
+    if (cfg->tensor_scale != MX_TS_NONE && !tensor_scale) return MX_ERR_INVALID;
+    if (cfg->macro_block && !macro_scales) return MX_ERR_INVALID;
+    if (cfg->asymmetric && !offsets) return MX_ERR_INVALID;
+    if (!aligned16(codes) || !aligned16(scales) || (cfg->macro_block && !aligned16(macro_scales)) ||
+        (cfg->asymmetric && !aligned16(offsets)) || (uintptr_t)x % xs ||
+        (cfg->tensor_scale != MX_TS_NONE && ((uintptr_t)tensor_scale & 3u)))
+        return MX_ERR_ALIGN;
+
+    GvParams p = {};
+    p.x = x;
+    p.ldx = ldx;
+    p.x_fp32 = x_dtype == MX_DT_FP32;
+    p.x_vec = aligned16(x) && (ldx * xs) % 16 == 0;
+    p.M = M;
+    p.N = N;
+    p.K = K;
+    p.codes = static_cast<const uint8_t *>(codes);
+    p.scales = scales;
+    p.ts = cfg->tensor_scale != MX_TS_NONE ? tensor_scale : nullptr;
+    p.macro = cfg->macro_block ? macro_scales : nullptr;
+    p.off = cfg->asymmetric ? offsets : nullptr;
+    p.S = K / cfg->block;
+    p.n_scales = N * p.S;
+    p.sf_chunk = cfg->sf_layout;
+    p.sfmt = cfg->scale_fmt;
+    while ((1 << p.log2B) < cfg->block) ++p.log2B;
+    p.elem = cfg->elem == MX_E2M1 ? GE_E2M1 : cfg->elem == MX_E3M0 ? GE_E3M0 : cfg->asymmetric ? GE_UINT4 : GE_INT4;
+    p.y = y;
+    p.ldy = ldy;
+    p.y_fp32 = y_dtype == MX_DT_FP32;
+    return launch_gemv(p, st) ? MX_ERR_CUDA : MX_OK;
 }
 
 int mx_tensor_amax(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t rows, int64_t cols,

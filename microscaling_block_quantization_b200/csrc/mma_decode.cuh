@@ -1,0 +1,144 @@
+// Pieces shared by the decode-time kernels (few activation rows against
+// block-scaled codes): 4-bit code words to f16 pairs, block scales to
+// binary32, the m16n8 matrix instructions and 16-byte asynchronous copies.
+//
+// Every element grid here is exact in f16, so the matrix instruction forms
+// exact products q x of a code value and an f16 activation piece and sums
+// them in binary32; the block scale multiplies that sum.
+#pragma once
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "mx_device.cuh"
+
+namespace mxk {
+
+// element kinds of a packed 4-bit word
+enum { GE_E2M1 = 0, GE_E3M0 = 1, GE_INT4 = 2, GE_UINT4 = 3 };
+
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Eight codes of a word -> four f16x2 of their grid values, codes (2i, 2i+1)
+// in h[i].  E2M1: the conversion instruction.  INT4: a byte's nibbles spread
+// to the two halves (multiply by 2^12 + 1, mask) under the exponent of 1024,
+// where an f16 ulp is 1, then 1024 (+ 8 for two's complement, whose sign bit
+// is flipped first) taken off: exact.  E3M0: the 3-bit magnitude is an f16
+// exponent field (0 -> 0), times 2^12.
+template <int ELEM>
+__device__ __forceinline__ void codes8_halves(uint32_t w, uint32_t h[4])
+{
+    if (ELEM == GE_E2M1) {
+        e2m1x8_halves(w, h);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = __byte_perm(w, 0u, 0x4440u + i);
+        if (ELEM == GE_E3M0) {
+            const uint32_t mag = (b * 0x00400400u) & 0x1c001c00u;   // b << 10 | b << 22
+            const uint32_t sgn = (b * 0x01001000u) & 0x80008000u;   // b << 12 | b << 24
+            h[i] = hmul2_u(mag | sgn, 0x6c006c00u);                 // 2^12
+        } else if (ELEM == GE_INT4) {
+            h[i] = hadd2_u(((b * 0x1001u) & 0x000f000fu) ^ 0x64086408u, 0xe408e408u);
+        } else {
+            h[i] = hadd2_u(((b * 0x1001u) & 0x000f000fu) ^ 0x64006400u, 0xe400e400u);
+        }
+    }
+}
+
+// Block-scale bytes -> binary32: four codes of a word.
+__device__ __forceinline__ void scales4(int fmt, uint32_t w, float s[4])
+{
+    if (fmt == S_E8M0) {
+        // 2^(code - 127), 0xFF -> NaN, code 0 -> 2^-127: exact in bf16
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+            "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+        s[0] = bits2f(lo << 16);
+        s[1] = bits2f(lo & 0xffff0000u);
+        s[2] = bits2f(hi << 16);
+        s[3] = bits2f(hi & 0xffff0000u);
+        return;
+    }
+    // unsigned minifloats with 3 mantissa bits: the byte shifted into a
+    // binary32 exponent and mantissa (subnormal codes become binary32
+    // subnormals), rescaled by an exact power of two
+    const float up = fmt == S_UE4M3 ? 0x1p120f : 0x1p112f;
+    const uint32_t nan_code = fmt == S_UE4M3 ? 0x7fu : 0xffu;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t b = (w >> (8 * i)) & 0xffu;
+        s[i] = b >= nan_code ? bits2f(0x7fc00000u) : __fmul_rn(bits2f(b << 20), up);
+    }
+}
+
+// D (16 x 8, binary32) += A (16 x 16, f16) B (16 x 8, f16); lane = 4 g + t
+// holds A rows g, g + 8 at k = 2t, 2t + 1 (a0, a1) and 2t + 8, 2t + 9 (a2,
+// a3), B column g at the same k, D rows g, g + 8 at columns 2t, 2t + 1.
+__device__ __forceinline__ void mma_16816(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// the same with 8 values of k
+__device__ __forceinline__ void mma_1688(float d[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// asynchronous global -> shared copies; bytes beyond src_bytes are zero
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int src_bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait()
+{
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t a)
+{
+    uint32_t r;
+    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a)
+{
+    uint4 r;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+
+// exponent of the power of two that brings amax into [2^14, 2^15) (f16
+// without overflow after rounding): 14 - floor(log2 amax).  An infinite or
+// NaN amax gives 2^-114: the finite values beside it no longer matter to the
+// sums it enters.  Below 2^-100 the scale stays at 2^114.
+__device__ __forceinline__ int f16_scale_exponent(float amax)
+{
+    const int e = (int)(__float_as_uint(amax) >> 23) - 127;
+    return 14 - max(e, -100);
+}
+
+}  // namespace mxk

@@ -20,6 +20,8 @@ constexpr int64_t kWsHeader = 256;
 // Largest tensor a call takes (elements, exclusive): the kernels index
 // elements, 8-element code words and blocks in 32 bits.
 constexpr int64_t kMaxElements = INT64_C(1) << 32;
+// Most rows x of an mx_gemv call (the launch grid's second dimension)
+constexpr int64_t kMaxGemvRows = INT64_C(1) << 17;
 constexpr int64_t kWsTicket = 64;
 // the MSE rule's tensor scale of each alternation round (floats, cleared by
 // the call that used them)
@@ -77,6 +79,25 @@ struct SParams {
     double *partials;
 };
 
+// mx_gemv: y[M][N] = x[M][K] (W^Q[N][K])^T
+struct GvParams {
+    const void *x;
+    int64_t ldx;
+    int x_fp32, x_vec;       // x_vec: rows start on 16-byte boundaries
+    int64_t M, N, K;
+    const uint8_t *codes, *scales;
+    const float *ts;         // tensor scale, or null
+    const uint8_t *macro;    // macro scales, or null
+    const uint16_t *off;     // block offsets, or null
+    int64_t S, n_scales;     // scales per row and in all
+    int sf_chunk, sfmt, log2B;
+    int elem;                // GE_* of mma_decode.cuh
+    void *y;
+    int64_t ldy;
+    int y_fp32;
+    int group, chunks;       // tokens of a launch row, 128-column chunks (set by launch_gemv)
+};
+
 // per-launch helpers implemented in the .cu files
 int launch_quantize(const QParams &p, int axis, int in_fp32, int fast, cudaStream_t st,
                     int *grid_out);
@@ -91,6 +112,11 @@ int device_sm_count();
 // the shared-memory attribute are host work that would otherwise sit between
 // short kernels); raises the kernel's dynamic shared-memory limit as needed.
 int cached_occupancy(const void *kernel, int threads, size_t smem);
+
+// Raise a kernel's dynamic shared-memory limit on the current device, once
+// per (kernel, device); 0 on success.
+int raise_smem_limit(const void *kernel, int bytes);
+int launch_gemv(GvParams p, cudaStream_t st);
 
 // Programmatic dependent launch: a CTA lets the next launch on the stream
 // start (its CTAs take SMs as this grid's CTAs retire) and, before its first

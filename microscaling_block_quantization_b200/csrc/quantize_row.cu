@@ -432,6 +432,22 @@ int cached_occupancy(const void *kernel, int threads, size_t smem)
     return occ;
 }
 
+int raise_smem_limit(const void *kernel, int bytes)
+{
+    struct Entry { const void *k; int dev, bytes; };
+    static Entry table[512];
+    static int used = 0;
+    static std::mutex mu;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return 1;
+    std::lock_guard<std::mutex> lock(mu);
+    for (int i = 0; i < used; ++i)
+        if (table[i].k == kernel && table[i].dev == dev && table[i].bytes >= bytes) return 0;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return 1;
+    if (used < 512) table[used++] = Entry{kernel, dev, bytes};
+    return 0;
+}
+
 static int g_sms = 0;
 int device_sm_count()
 {
