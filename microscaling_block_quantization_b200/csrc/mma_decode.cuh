@@ -57,7 +57,18 @@ __device__ __forceinline__ void codes8_halves(uint32_t w, uint32_t h[4])
     }
 }
 
-// Block-scale bytes -> binary32: four codes of a word.
+// A block-scale code -> binary32.  Unsigned minifloats with 3 mantissa bits:
+// the byte shifted into an exponent and mantissa, rescaled by an exact power
+// of two.
+__device__ __forceinline__ float scale1(int fmt, uint32_t b)
+{
+    if (fmt == S_E8M0) return b == 0xffu ? bits2f(0x7fc00000u) : b ? bits2f(b << 23) : bits2f(0x00400000u);
+    const float up = fmt == S_UE4M3 ? 0x1p120f : 0x1p112f;
+    const uint32_t nan_code = fmt == S_UE4M3 ? 0x7fu : 0xffu;
+    return b >= nan_code ? bits2f(0x7fc00000u) : __fmul_rn(bits2f(b << 20), up);
+}
+
+// Four codes of a word.
 __device__ __forceinline__ void scales4(int fmt, uint32_t w, float s[4])
 {
     if (fmt == S_E8M0) {
@@ -74,16 +85,26 @@ __device__ __forceinline__ void scales4(int fmt, uint32_t w, float s[4])
         s[3] = bits2f(hi & 0xffff0000u);
         return;
     }
-    // unsigned minifloats with 3 mantissa bits: the byte shifted into a
-    // binary32 exponent and mantissa (subnormal codes become binary32
-    // subnormals), rescaled by an exact power of two
-    const float up = fmt == S_UE4M3 ? 0x1p120f : 0x1p112f;
-    const uint32_t nan_code = fmt == S_UE4M3 ? 0x7fu : 0xffu;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t b = (w >> (8 * i)) & 0xffu;
-        s[i] = b >= nan_code ? bits2f(0x7fc00000u) : __fmul_rn(bits2f(b << 20), up);
+    if (fmt == S_UE4M3) {
+        // the E4M3 conversion (0x7F is its NaN); bytes from 0x80 on, which no
+        // finite scale has, are NaN too
+        const uint32_t top = w & 0x80808080u;
+        if (top) w |= (top >> 7) * 0x7fu;
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+        const float2 a = __half22float2(*reinterpret_cast<const __half2 *>(&lo));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+        s[0] = a.x; s[1] = a.y; s[2] = b.x; s[3] = b.y;
+        return;
     }
+    // UE5M3: the byte shifted into a binary32 exponent and mantissa
+    // (subnormal codes become binary32 subnormals), rescaled exactly
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = scale1(fmt, (w >> (8 * i)) & 0xffu);
 }
 
 // D (16 x 8, binary32) += A (16 x 16, f16) B (16 x 8, f16); lane = 4 g + t
@@ -96,11 +117,19 @@ __device__ __forceinline__ void mma_16816(float d[4], uint32_t a0, uint32_t a1, 
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// the same with 8 values of k
-__device__ __forceinline__ void mma_1688(float d[4], uint32_t a0, uint32_t a1, uint32_t b0)
+// the same from zero
+__device__ __forceinline__ void mma_16816_zero(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                               uint32_t b0, uint32_t b1)
 {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(b0));
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+// 8 values of k, from zero
+__device__ __forceinline__ void mma_1688_zero(float d[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%7,%7,%7,%7};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
 }
 
 // asynchronous global -> shared copies; bytes beyond src_bytes are zero
@@ -122,6 +151,12 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a)
 {
     uint32_t r;
     asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t r;
+    asm volatile("ld.shared.b16 %0, [%1];" : "=h"(r) : "r"(a));
     return r;
 }
 __device__ __forceinline__ uint4 lds128(uint32_t a)
