@@ -444,6 +444,58 @@ int mx_gemv(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t ldx, i
             const uint8_t *scales, const float *tensor_scale, const uint8_t *macro_scales, const uint16_t *offsets,
             int64_t N, int64_t K, void *y, int32_t y_dtype, int64_t ldy, void *stream);
 
+/* A paged cache of attention keys and values in a block-scaled format: one row
+ * per token of kv_heads * head_dim elements, in mx_quantize's canonical row
+ * layout (codes, then one scale byte per block along the head), so that
+ * mx_quantize and mx_dequantize read and write whole pages of it too.  Page n
+ * holds rows [n page_size, (n + 1) page_size).  The caller owns the buffers
+ * (codes: rows * cols / 2 bytes, FP6 rows * cols; scales: rows * cols / block).
+ * Configurations: row axis, canonical scales, symmetric, blocks of 16, 32, 64 or
+ * 128 and at most head_dim, RTNE or ceil rounding, any element type and any rule
+ * but MSE;
+ * tensor_scale MX_TS_NONE or MX_TS_GIVEN (one scale for keys, one for values).
+ * head_dim 64, 128 or 256; any page_size >= 1; fewer than 2^31 rows; the cache may
+ * pass 2^32 elements. */
+typedef struct {
+    void *k_codes, *v_codes;
+    uint8_t *k_scales, *v_scales;
+    const float *k_tensor_scale, *v_tensor_scale;   /* device floats (MX_TS_GIVEN) */
+    int64_t pages;
+    int32_t page_size, kv_heads, head_dim;
+} mx_kv_cache;
+
+/*
+ * mx_kv_append -- queries, keys and values of new tokens made ready for
+ * attention over a block-scaled cache, in one pass: RMS norm of every query
+ * and key head, position rotation, and the keys and values quantized into
+ * cache rows (as the rotation of [BRIDGING] sec. 2.3 is fused with its
+ * quantizer; the norm and the position rotation are standard parts of a
+ * transformer layer that the pages do not describe).
+ *   h = x / sqrt(sum x^2 / head_dim + eps) * gain   (when the gain is given);
+ *   element pairs (i, i + rot_dim / 2) -- or (2i, 2i + 1) when interleaved --
+ *   of the first rot_dim elements are turned by position * inv_freq[i]
+ *   (a cos - b sin, b cos + a sin; the angle in binary64); each result is
+ *   rounded once to dtype.  Keys so rounded and values as given are quantized:
+ *   the rows hold what mx_quantize writes for them, bit for bit.
+ *   q, k, v      device, bf16 or fp32 (dtype); token t's heads are contiguous
+ *                at q + t ldq elements, and so on (slices of one fused
+ *                projection are fine).  q may be NULL with q_heads == 0.
+ *   q_gain, k_gain   device, fp32 [head_dim], 16-byte aligned, or NULL (no norm).
+ *   inv_freq     device, fp32 [rot_dim / 2]; positions: device, int64 per token.
+ *                rot_dim % 16 == 0; 0: no rotation.
+ *   slots        device, int64 per token: the cache row its key and value go to;
+ *                a slot outside the cache (-1 for padding) stores nothing.  Slots of
+ *                one call must differ: two tokens with one slot leave a mixture.
+ *   q_out        device, dtype; may be q itself (same ld).  k_out: the rotated
+ *                keys in dtype, or NULL; may be k itself.
+ * One launch, no workspace; rows that no slot names stay as they were.
+ */
+int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, const void *k, const void *v,
+                 int32_t dtype, int64_t ldq, int64_t ldk, int64_t ldv, int64_t tokens, int32_t q_heads,
+                 const float *q_gain, const float *k_gain, float eps, const float *inv_freq, int32_t rot_dim,
+                 int32_t interleaved, const int64_t *positions, const int64_t *slots, void *q_out, int64_t ldqo,
+                 void *k_out, int64_t ldko, void *stream);
+
 /*
  * mx_tensor_peak -- tensor-core ceiling probe for the roofline of mx_gemm (the
  * pages have no counterpart; it measures the device, not the method).  One

@@ -55,6 +55,12 @@ class mx_quantize_item(C.Structure):
                 ("workspace_bytes", C.c_int64)]
 
 
+class mx_kv_cache(C.Structure):
+    _fields_ = [("k_codes", C.c_void_p), ("v_codes", C.c_void_p), ("k_scales", C.c_void_p), ("v_scales", C.c_void_p),
+                ("k_tensor_scale", C.c_void_p), ("v_tensor_scale", C.c_void_p), ("pages", C.c_int64),
+                ("page_size", C.c_int32), ("kv_heads", C.c_int32), ("head_dim", C.c_int32)]
+
+
 class mx_sizes(C.Structure):
     _fields_ = [("codes_bytes", C.c_int64), ("n_scales", C.c_int64), ("n_macro", C.c_int64),
                 ("n_offsets", C.c_int64), ("workspace_bytes", C.c_int64), ("n_blocks", C.c_int64)]
@@ -128,6 +134,8 @@ def lib() -> C.CDLL:
         L.mx_gemm.argtypes = [cfgp, cfgp, P, P, P, P, P, P, i64, i64, i64, P, i32, P]
         L.mx_gemm_qsnr.argtypes = [cfgp, cfgp, P, P, i64, i64, i64, P, P, P, P, P, P, P, P, i64, P]
         L.mx_gemv.argtypes = [cfgp, P, i32, i64, i64, P, P, P, P, P, i64, i64, P, i32, i64, P]
+        L.mx_kv_append.argtypes = [cfgp, C.POINTER(mx_kv_cache), P, P, P, i32, i64, i64, i64, i64, i32, P, P, C.c_float, P, i32,
+                                   i32, P, P, P, i64, P, i64, P]
         L.mx_mbs_gemm_scales.argtypes = [cfgp, P, P, i64, i64, P, P, P, i64, P]
         L.mx_device_status.argtypes = [P, C.POINTER(i32)]
         L.mx_tensor_amax.argtypes = [cfgp, P, i32, i64, i64, P, i64, P]
@@ -139,7 +147,7 @@ def lib() -> C.CDLL:
         L.mx_version.restype = C.c_char_p
         for f in ("mx_query_sizes", "mx_quantize", "mx_quantize_group", "mx_quantize_noalloc",
                   "mx_hadamard_quantize", "mx_dequantize",
-                  "mx_qsnr", "mx_gemm", "mx_gemv", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
+                  "mx_qsnr", "mx_gemm", "mx_gemv", "mx_kv_append", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
                   "mx_tensor_amax", "mx_stats_finalize", "mx_gemm_qsnr_finalize", "mx_tensor_peak"):
             getattr(L, f).restype = C.c_int
         _lib = L
@@ -261,6 +269,13 @@ def mx_gemv(cfg: Config, x, x_dtype, ldx, M, codes, scales, tensor_scale, macro,
             ldy, stream) -> int:
     return lib().mx_gemv(cfg.ref(), x, x_dtype, ldx, M, codes, scales, tensor_scale, macro, offsets, N, K, y,
                          y_dtype, ldy, stream)
+
+
+def mx_kv_append(cfg: Config, cache, q, k, v, dtype, ldq, ldk, ldv, tokens, q_heads, q_gain, k_gain, eps, inv_freq,
+                 rot_dim, interleaved, positions, slots, q_out, ldqo, k_out, ldko, stream) -> int:
+    """``cache``: an ``mx_kv_cache`` by reference."""
+    return lib().mx_kv_append(cfg.ref(), cache, q, k, v, dtype, ldq, ldk, ldv, tokens, q_heads, q_gain, k_gain, eps,
+                              inv_freq, rot_dim, interleaved, positions, slots, q_out, ldqo, k_out, ldko, stream)
 
 
 def mx_gemm_qsnr(ca: Config, cb: Config, A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB, stats,
@@ -574,6 +589,133 @@ def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *
                      y.data_ptr(), _DT[y.dtype], ldy, st)
     _check("mx_gemv", rc)
     return out if out is not None else y if x.dim() == 2 else y[0]
+
+
+@dataclasses.dataclass
+class KVCache:
+    """A paged cache of attention keys and values in a block-scaled format:
+    ``pages * page_size`` rows of ``kv_heads * head_dim`` elements, ``k`` and ``v`` as
+    ``quantize`` would hold such a tensor (``dequantize(cache.k)`` reads it back).
+    The buffers must stay those the cache was made with."""
+    cfg: Config
+    pages: int
+    page_size: int
+    kv_heads: int
+    head_dim: int
+    k: Quantized
+    v: Quantized
+
+    def ref(self):
+        """The C struct by reference, built once per cache."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            rows, cols, bits = self.pages * self.page_size, self.kv_heads * self.head_dim, 8 if self.cfg.elem in FP6 else 4
+            for name, t in (("k", self.k), ("v", self.v)):
+                _same_device(self.device, **{name + ".scales": t.scales, name + ".codes": t.codes,
+                                             name + ".tensor_scale": t.tensor_scale if self.cfg.tensor_scale else None})
+                if (t.codes.numel() * t.codes.element_size() < rows * cols * bits // 8 or not t.codes.is_contiguous() or
+                        t.scales.numel() < rows * (cols // self.cfg.block) or not t.scales.is_contiguous()):
+                    raise ValueError(f"{name}: buffers too small for {rows} rows of {cols}, or not contiguous")
+                if self.cfg.tensor_scale and (t.tensor_scale is None or t.tensor_scale.dtype != torch.float32):
+                    raise TypeError(f"{name}: a float32 tensor scale is needed")
+            ts = [t.tensor_scale.data_ptr() if self.cfg.tensor_scale else None for t in (self.k, self.v)]
+            r = C.byref(mx_kv_cache(self.k.codes.data_ptr(), self.v.codes.data_ptr(), self.k.scales.data_ptr(),
+                                    self.v.scales.data_ptr(), ts[0], ts[1], self.pages, self.page_size, self.kv_heads,
+                                    self.head_dim))
+            self.__dict__["_ref"] = r
+        return r
+
+    @property
+    def device(self):
+        return self.k.codes.device
+
+
+def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, cfg: Config = MXFP4, *, device="cuda",
+             k_tensor_scale: torch.Tensor | None = None, v_tensor_scale: torch.Tensor | None = None) -> KVCache:
+    """A cache of zeros.  With ``cfg.tensor_scale == TS_GIVEN`` the two tensor
+    scales (float32[1] on the device) are needed."""
+    rows, cols = pages * page_size, kv_heads * head_dim
+    dev = torch.device(device)
+    if dev.type == "cuda" and dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+
+    def half(ts):
+        codes = torch.zeros(max(16, rows * cols // (1 if cfg.elem in FP6 else 2)), dtype=torch.uint8, device=dev)
+        scales = torch.zeros(max(16, rows * cols // cfg.block), dtype=torch.uint8, device=dev)
+        return Quantized(cfg, rows, cols, codes, scales, ts, None, None, None)
+
+    if cfg.tensor_scale and (k_tensor_scale is None or v_tensor_scale is None):
+        raise ValueError("this configuration needs k_tensor_scale and v_tensor_scale")
+    return KVCache(cfg, pages, page_size, kv_heads, head_dim, half(k_tensor_scale), half(v_tensor_scale))
+
+
+def _heads(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
+    """Token stride of ``[T, heads * dim]`` or ``[T, heads, dim]`` with contiguous heads."""
+    if t.dim() == 3 and tuple(t.shape[1:]) == (heads, dim):
+        if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+            raise ValueError(f"the heads of {name} must be contiguous")
+    elif not (t.dim() == 2 and t.shape[1] == heads * dim and t.stride(1) == 1):
+        raise ValueError(f"{name} must be [T, {heads * dim}] or [T, {heads}, {dim}] with contiguous heads, got "
+                         f"{list(t.shape)} with strides {t.stride()}")
+    if t.shape[0] > 1 and t.stride(0) < heads * dim:
+        raise ValueError(f"the tokens of {name} overlap")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _vector(t, n, dtype, device, name):
+    """Pointer of an optional contiguous vector."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be {n} contiguous {dtype} on {device}")
+    return t.data_ptr()
+
+
+def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+              positions: torch.Tensor | None = None, *, q_gain: torch.Tensor | None = None,
+              k_gain: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
+              interleaved: bool = False, q_out: torch.Tensor | None = None, k_out=False, stream=None):
+    """Per-head RMS norm (``q_gain`` / ``k_gain``, fp32 ``[head_dim]``) and position
+    rotation (``positions`` int64 ``[T]``, ``inv_freq`` fp32 ``[rot / 2]``) of new tokens'
+    queries and keys, and their keys and values quantized into the cache rows
+    ``slots`` (int64 ``[T]``, -1: not stored), in one pass (``mx_kv_append``).  q, k,
+    v: ``[T, heads * head_dim]`` or ``[T, heads, head_dim]``, tokens at any stride (slices of a
+    fused projection).  Returns ``(q_out, k_out)``: the rotated queries
+    ``[T, q_heads, head_dim]`` (into ``q_out`` when given; it may be q) and, when ``k_out`` is
+    True or a tensor, the rotated keys, else None."""
+    if not k.is_cuda:
+        raise ValueError("k must be a CUDA tensor")
+    D, H, T, dev = cache.head_dim, cache.kv_heads, k.shape[0], cache.device
+    if k.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {k.dtype} (bf16 or fp32)")
+    _same_device(dev, k=k, v=v, q=q, q_out=q_out, k_out=k_out if isinstance(k_out, torch.Tensor) else None)
+    ldk, ldv = _heads(k, H, D, "k"), _heads(v, H, D, "v")
+    Hq = 0 if q is None else q.shape[1] if q.dim() == 3 else q.shape[1] // D
+    ldq = 0 if q is None else _heads(q, Hq, D, "q")
+    for name, t in (("v", v), ("q", q), ("q_out", q_out), ("k_out", k_out if isinstance(k_out, torch.Tensor) else None)):
+        if t is not None and (t.dtype != k.dtype or t.shape[0] != T):
+            raise ValueError(f"{name} must have {T} tokens of {k.dtype}")
+    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
+    if rot and positions is None:
+        raise ValueError("a rotation needs positions")
+    ps = _vector(positions, T, torch.int64, dev, "positions")
+    pf = _vector(inv_freq, rot // 2, torch.float32, dev, "inv_freq")
+    pq, pk = _vector(q_gain, D, torch.float32, dev, "q_gain"), _vector(k_gain, D, torch.float32, dev, "k_gain")
+    pl = _vector(slots, T, torch.int64, dev, "slots")
+    with _Launch(dev, stream) as st:
+        if q is not None and q_out is None:
+            q_out = torch.empty((T, Hq, D), dtype=k.dtype, device=dev)
+        if k_out is True:
+            k_out = torch.empty((T, H, D), dtype=k.dtype, device=dev)
+        elif k_out is False:
+            k_out = None
+        ldqo = 0 if q_out is None else _heads(q_out, Hq, D, "q_out")
+        ldko = 0 if k_out is None else _heads(k_out, H, D, "k_out")
+        rc = mx_kv_append(cache.cfg, cache.ref(), _ptr_or_none(q), k.data_ptr(), v.data_ptr(), _DT[k.dtype], ldq, ldk, ldv,
+                          T, Hq, pq, pk, eps, pf, rot, int(interleaved), ps, pl, _ptr_or_none(q_out), ldqo,
+                          _ptr_or_none(k_out), ldko, st)
+    _check("mx_kv_append", rc)
+    return q_out, k_out
 
 
 def mbs_gemm_operand(q: Quantized, stream=None) -> Quantized:

@@ -291,6 +291,34 @@ bool col_groupable(const mx_config *cfg, int32_t x_dtype)
            !cfg->hadamard;
 }
 
+// A cache of attention keys and values: one row per token of kv_heads * head_dim
+// elements, quantized along the head.
+int check_cache(const mx_config *cfg, const mx_kv_cache *c)
+{
+    if (!cfg || !c) return MX_ERR_INVALID;
+    if (c->kv_heads < 1 || c->kv_heads > 4096 || c->page_size < 1 || c->pages < 0) return MX_ERR_INVALID;
+    if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return MX_ERR_UNSUPPORTED;
+    if (c->pages > INT32_MAX || c->pages * (int64_t)c->page_size > INT32_MAX) return MX_ERR_INVALID;
+    int rc = check_config(cfg, 0, 0, cfg->hadamard != 0);
+    if (rc != MX_OK) return rc;
+    if (cfg->axis != MX_AXIS_ROW || cfg->sf_layout || cfg->asymmetric || cfg->macro_block || cfg->hadamard ||
+        cfg->rule == MX_RULE_MSE || cfg->round == MX_ROUND_STOCHASTIC || cfg->block < 16 || cfg->block > 128 ||
+        cfg->block > c->head_dim ||
+        cfg->tensor_scale == MX_TS_COMPUTE || cfg->tensor_scale == MX_TS_AMAX)
+        return MX_ERR_UNSUPPORTED;
+    rc = check_config(cfg, 1, (int64_t)c->kv_heads * c->head_dim, false);
+    if (rc != MX_OK) return rc;
+    if (c->pages == 0) return MX_OK;
+    if (!c->k_codes || !c->v_codes || !c->k_scales || !c->v_scales) return MX_ERR_INVALID;
+    if (!aligned16(c->k_codes) || !aligned16(c->v_codes) || !aligned16(c->k_scales) || !aligned16(c->v_scales))
+        return MX_ERR_ALIGN;
+    if (cfg->tensor_scale != MX_TS_NONE) {
+        if (!c->k_tensor_scale || !c->v_tensor_scale) return MX_ERR_INVALID;
+        if (((uintptr_t)c->k_tensor_scale & 3u) || ((uintptr_t)c->v_tensor_scale & 3u)) return MX_ERR_ALIGN;
+    }
+    return MX_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -465,6 +493,74 @@ int mx_gemv(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t ldx, i
     p.ldy = ldy;
     p.y_fp32 = y_dtype == MX_DT_FP32;
     return launch_gemv(p, st) ? MX_ERR_CUDA : MX_OK;
+}
+
+int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, const void *k, const void *v,
+                 int32_t dtype, int64_t ldq, int64_t ldk, int64_t ldv, int64_t tokens, int32_t q_heads,
+                 const float *q_gain, const float *k_gain, float eps, const float *inv_freq, int32_t rot_dim,
+                 int32_t interleaved, const int64_t *positions, const int64_t *slots, void *q_out, int64_t ldqo,
+                 void *k_out, int64_t ldko, void *stream)
+{
+    const int rc = check_cache(cfg, cache);
+    if (rc != MX_OK) return rc;
+    if (dtype != MX_DT_BF16 && dtype != MX_DT_FP32) return MX_ERR_INVALID;
+    if (tokens < 0 || q_heads < 0 || q_heads > 65536 || (interleaved != 0 && interleaved != 1)) return MX_ERR_INVALID;
+    if (rot_dim < 0 || rot_dim > cache->head_dim) return MX_ERR_INVALID;
+    if (rot_dim % 16) return MX_ERR_UNSUPPORTED;
+    if ((q_gain || k_gain) && !(eps >= 0.0f && eps < INFINITY)) return MX_ERR_INVALID;
+    if (tokens == 0) return MX_OK;
+    const int64_t D = cache->head_dim, cols = cache->kv_heads * D;
+    if (!k || !v || !slots || (q_heads && (!q || !q_out)) || (rot_dim && (!inv_freq || !positions))) return MX_ERR_INVALID;
+    if (ldk < cols || ldv < cols || (q_heads && (ldq < q_heads * D || ldqo < q_heads * D)) || (k_out && ldko < cols))
+        return MX_ERR_INVALID;
+    const int es = dtype == MX_DT_FP32 ? 4 : 2;
+    const void *ptrs[] = {k, v, k_out, q_heads ? q : nullptr, q_heads ? q_out : nullptr};
+    for (const void *ptr : ptrs)
+        if ((uintptr_t)ptr % es) return MX_ERR_ALIGN;
+    if (!aligned16(q_gain) || !aligned16(k_gain) || ((uintptr_t)inv_freq & 3u) || ((uintptr_t)positions & 7u) ||
+        ((uintptr_t)slots & 7u))
+        return MX_ERR_ALIGN;
+
+    KvAppendParams p = {};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.ldq = ldq;
+    p.ldk = ldk;
+    p.ldv = ldv;
+    p.tokens = tokens;
+    p.q_heads = q_heads;
+    p.kv_heads = cache->kv_heads;
+    p.cols = (int)cols;
+    p.q_gain = q_gain;
+    p.k_gain = k_gain;
+    p.eps = eps;
+    p.inv_freq = inv_freq;
+    p.rot = rot_dim;
+    p.interleaved = interleaved;
+    p.positions = positions;
+    p.slots = slots;
+    p.cache_rows = cache->pages * cache->page_size;
+    p.q_out = q_out;
+    p.k_out = k_out;
+    p.ldqo = ldqo;
+    p.ldko = ldko;
+    const auto rows16 = [es](const void *b, int64_t ld) { return aligned16(b) && (ld * es) % 16 == 0; };
+    p.in_vec = (!q_heads || rows16(q, ldq)) && rows16(k, ldk) && rows16(v, ldv);
+    p.out_vec = (!q_heads || rows16(q_out, ldqo)) && (!k_out || rows16(k_out, ldko));
+    p.k_codes = static_cast<uint8_t *>(cache->k_codes);
+    p.v_codes = static_cast<uint8_t *>(cache->v_codes);
+    p.k_scales = cache->k_scales;
+    p.v_scales = cache->v_scales;
+    p.k_ts = cfg->tensor_scale != MX_TS_NONE ? cache->k_tensor_scale : nullptr;
+    p.v_ts = cfg->tensor_scale != MX_TS_NONE ? cache->v_tensor_scale : nullptr;
+    if (!make_elem(cfg->elem, 0, p.ed) || !make_scale(cfg, p.sd)) return MX_ERR_INVALID;
+    p.round_mode = cfg->round;
+    p.lanes_per_block = cfg->block / 8;
+    while ((1 << p.log2B) < cfg->block) ++p.log2B;
+    const float thr = cfg->rule == MX_RULE_CEIL ? p.ed.maxv : cfg->rule == MX_RULE_OAS ? cfg->oas_tau : INFINITY;
+    p.thr_m = ldexpf(thr, -p.ed.emax);
+    return launch_kv_append(p, cache->head_dim, dtype == MX_DT_FP32, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;
 }
 
 int mx_tensor_amax(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t rows, int64_t cols,

@@ -98,6 +98,30 @@ struct GvParams {
     int group, chunks;       // tokens of a launch row, 128-column chunks (set by launch_gemv)
 };
 
+// mx_kv_append: tokens' queries, keys and values, cache rows out
+struct KvAppendParams {
+    const void *q, *k, *v;
+    int64_t ldq, ldk, ldv;   // elements between tokens
+    int64_t tokens;
+    int q_heads, kv_heads, cols;   // cols = kv_heads * head_dim
+    const float *q_gain, *k_gain;
+    float eps;
+    const float *inv_freq;
+    int rot, interleaved;
+    const int64_t *positions, *slots;
+    int64_t cache_rows;
+    void *q_out, *k_out;
+    int64_t ldqo, ldko;
+    int in_vec, out_vec;     // every row starts on a 16-byte boundary
+    uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    const float *k_ts, *v_ts;
+    ElemDesc ed;
+    ScaleDesc sd;
+    int round_mode, lanes_per_block, log2B;
+    float thr_m;             // e8m0_threshold of the rule
+    int group;               // tokens whose angles a CTA holds (set by the launch)
+};
+
 // per-launch helpers implemented in the .cu files
 int launch_quantize(const QParams &p, int axis, int in_fp32, int fast, cudaStream_t st,
                     int *grid_out);
@@ -117,6 +141,7 @@ int cached_occupancy(const void *kernel, int threads, size_t smem);
 // per (kernel, device); 0 on success.
 int raise_smem_limit(const void *kernel, int bytes);
 int launch_gemv(GvParams p, cudaStream_t st);
+int launch_kv_append(KvAppendParams p, int head_dim, int in_fp32, cudaStream_t st);
 
 // Programmatic dependent launch: a CTA lets the next launch on the stream
 // start (its CTAs take SMs as this grid's CTAs retire) and, before its first

@@ -62,3 +62,70 @@ def test_gemv_binding_refusals(mx):
     q = mx.Quantized(mx.MXFP4, 4, 64, *(torch.zeros(16, dtype=torch.uint8) for _ in range(2)), torch.ones(1), None, None, None)
     with pytest.raises(ValueError):
         mx.gemv(torch.zeros(1, 64), q)                       # not on a CUDA device
+
+
+def cache(mx, pages=4, page_size=16, kv=2, dim=64, k=4096, v=4096, ks=4096, vs=4096, kt=4096, vt=4096):
+    return C.byref(mx.mx_kv_cache(k, v, ks, vs, kt, vt, pages, page_size, kv, dim))
+
+
+def append(mx, cfg, c, q=4096, k=4096, v=4096, dt=0, ldq=None, ldk=128, ldv=128, T=3, Hq=4, gq=4096, gk=4096, eps=1e-6,
+           freq=4096, rot=64, inter=0, pos=4096, slots=4096, qo=4096, ldqo=256, ko=None, ldko=128):
+    p = lambda x: None if x is None else P(x)  # noqa: E731
+    return mx.mx_kv_append(cfg, c, p(q), p(k), p(v), dt, 256 if ldq is None else ldq, ldk, ldv, T, Hq, p(gq), p(gk), eps,
+                           p(freq), rot, inter, p(pos), p(slots), p(qo), ldqo, p(ko), ldko, None)
+
+
+CACHE_CONFIGS = [
+    (dict(block=8), -2), (dict(block=256), -2), (dict(block=128), -2),      # 128 is longer than the head
+    (dict(axis=2), -2), (dict(axis=1, block=8), -2), (dict(sf_layout=1), -2), (dict(asymmetric=1), -2), (dict(macro_block=128), -2),
+    (dict(hadamard=32), -2), (dict(rule=4), -2), (dict(round=2), -2),
+    (dict(block=16, scale_fmt=1, rule=3, tensor_scale=1), -2), (dict(block=16, scale_fmt=1, rule=3, tensor_scale=3), -2),
+    (dict(elem=9), -1), (dict(rule=3), -1),
+]
+CACHES = [
+    (dict(dim=96), -2), (dict(kv=0), -1), (dict(page_size=0), -1), (dict(pages=-1), -1), (dict(pages=1 << 30, page_size=2), -1),
+    (dict(k=None), -1), (dict(v=None), -1), (dict(ks=None), -1), (dict(vs=None), -1),
+    (dict(k=4104), -3), (dict(v=4104), -3), (dict(ks=4104), -3), (dict(vs=4100), -3),
+]
+
+
+@pytest.mark.parametrize("cfg,rc", CACHE_CONFIGS)
+def test_append_configurations(mx, cfg, rc):
+    assert append(mx, mx.Config(**cfg), cache(mx)) == rc
+
+
+@pytest.mark.parametrize("args,rc", CACHES)
+def test_append_caches(mx, args, rc):
+    assert append(mx, mx.MXFP4, cache(mx, **args)) == rc
+
+
+@pytest.mark.parametrize("args,rc", [
+    (dict(dt=2), -1), (dict(T=-1), -1), (dict(Hq=-1), -1), (dict(inter=2), -1), (dict(rot=80), -1), (dict(rot=24), -2),
+    (dict(eps=-1.0), -1), (dict(eps=float("nan")), -1), (dict(eps=float("inf")), -1),
+    (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(qo=None), -1), (dict(slots=None), -1), (dict(pos=None), -1),
+    (dict(freq=None), -1), (dict(ldq=255), -1), (dict(ldk=127), -1), (dict(ldv=0), -1), (dict(ldqo=255), -1), (dict(ko=4096, ldko=1), -1),
+    (dict(q=4097), -3), (dict(k=4097), -3), (dict(v=4098, dt=1), -3), (dict(ko=4097), -3), (dict(gq=4100), -3), (dict(gk=4104), -3),
+    (dict(freq=4098), -3), (dict(pos=4100), -3), (dict(slots=4100), -3), (dict(T=0), 0),
+])
+def test_append_arguments(mx, args, rc):
+    assert append(mx, mx.MXFP4, cache(mx), **args) == rc
+
+
+def test_append_tensor_scales(mx):
+    nv = mx.Config(block=16, scale_fmt=1, rule=3, tensor_scale=2)
+    assert append(mx, nv, cache(mx, kt=None)) == -1 and append(mx, nv, cache(mx, vt=None)) == -1
+    assert append(mx, nv, cache(mx, vt=4098)) == -3
+    assert append(mx, nv, None) == -1
+
+
+def test_append_binding_refusals(mx):
+    import torch
+    c = mx.kv_cache(2, 4, 1, 64, device="cpu")
+    with pytest.raises(ValueError):
+        mx.kv_append(c, None, torch.zeros(1, 64), torch.zeros(1, 64), torch.zeros(1, dtype=torch.int64))
+    with pytest.raises(ValueError):
+        mx.kv_cache(2, 4, 1, 64, mx.Config(block=16, scale_fmt=1, rule=3, tensor_scale=2), device="cpu")
+    small = mx.kv_cache(2, 4, 1, 64, device="cpu")
+    small.k.codes = small.k.codes[:8]
+    with pytest.raises(ValueError):
+        small.ref()
