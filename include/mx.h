@@ -497,6 +497,38 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
                  void *k_out, int64_t ldko, void *stream);
 
 /*
+ * mx_attn_decode -- attention of one query token per sequence over a paged
+ * block-scaled cache (standard decode attention, which the pages do not
+ * describe, on their formats): out_h = softmax(scale q_h K^T) V over the visible
+ * tokens, K and V as mx_dequantize would read the cache.
+ *   q            device, bf16 or fp32 (q_dtype): sequence s's q_heads heads of
+ *                head_dim contiguous at q + s ldq elements.  Query head h reads
+ *                key head h / (q_heads / kv_heads).
+ *   page_table   device, int32: entry j of row s (at s ld_table + j, j < max_pages)
+ *                is the page of the sequence's tokens [j page_size, (j + 1) page_size).
+ *                The tokens of an entry outside [0, pages) are not visible.
+ *   lengths      device, int32: the sequence's tokens, the query's own included
+ *                (clamped to [0, max_pages page_size]).
+ *   window       0: every token is visible.  Else the last `window` tokens and
+ *                the first `sinks`.
+ *   out          device, bf16 or fp32 (out_dtype), as q with ldo; lse: fp32
+ *                [seqs][q_heads], log sum exp of the scaled scores, or NULL.  A
+ *                sequence without a visible token gives zeros and -inf.
+ *   workspace    mx_attn_workspace_bytes() bytes, 16-byte aligned, not
+ *                initialised; calls that may run at the same time need their own.
+ * Scores, softmax statistics and sums are binary32; the weights are rounded to
+ * 11 bits for bf16 results and to 22 when q or out is fp32.  One launch, two
+ * where sequences are split; the split goes by the sizes given on the host,
+ * so results do not depend on timing.
+ */
+int64_t mx_attn_workspace_bytes(const mx_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_pages, int32_t window,
+                                int32_t sinks);
+int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q, int32_t q_dtype, int64_t ldq,
+                   int64_t seqs, int32_t q_heads, const int32_t *page_table, int64_t ld_table, int64_t max_pages,
+                   const int32_t *lengths, float scale, int32_t window, int32_t sinks, void *out, int32_t out_dtype,
+                   int64_t ldo, float *lse, void *workspace, int64_t workspace_bytes, void *stream);
+
+/*
  * mx_tensor_peak -- tensor-core ceiling probe for the roofline of mx_gemm (the
  * pages have no counterpart; it measures the device, not the method).  One
  * CTA per SM issues `iters` stages of four 128 x 256 x K block-scaled MMAs of

@@ -136,6 +136,10 @@ def lib() -> C.CDLL:
         L.mx_gemv.argtypes = [cfgp, P, i32, i64, i64, P, P, P, P, P, i64, i64, P, i32, i64, P]
         L.mx_kv_append.argtypes = [cfgp, C.POINTER(mx_kv_cache), P, P, P, i32, i64, i64, i64, i64, i32, P, P, C.c_float, P, i32,
                                    i32, P, P, P, i64, P, i64, P]
+        L.mx_attn_workspace_bytes.argtypes = [C.POINTER(mx_kv_cache), i64, i32, i64, i32, i32]
+        L.mx_attn_workspace_bytes.restype = i64
+        L.mx_attn_decode.argtypes = [cfgp, C.POINTER(mx_kv_cache), P, i32, i64, i64, i32, P, i64, i64, P, C.c_float, i32, i32, P,
+                                     i32, i64, P, P, i64, P]
         L.mx_mbs_gemm_scales.argtypes = [cfgp, P, P, i64, i64, P, P, P, i64, P]
         L.mx_device_status.argtypes = [P, C.POINTER(i32)]
         L.mx_tensor_amax.argtypes = [cfgp, P, i32, i64, i64, P, i64, P]
@@ -147,7 +151,7 @@ def lib() -> C.CDLL:
         L.mx_version.restype = C.c_char_p
         for f in ("mx_query_sizes", "mx_quantize", "mx_quantize_group", "mx_quantize_noalloc",
                   "mx_hadamard_quantize", "mx_dequantize",
-                  "mx_qsnr", "mx_gemm", "mx_gemv", "mx_kv_append", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
+                  "mx_qsnr", "mx_gemm", "mx_gemv", "mx_kv_append", "mx_attn_decode", "mx_gemm_qsnr", "mx_mbs_gemm_scales", "mx_device_status",
                   "mx_tensor_amax", "mx_stats_finalize", "mx_gemm_qsnr_finalize", "mx_tensor_peak"):
             getattr(L, f).restype = C.c_int
         _lib = L
@@ -276,6 +280,13 @@ def mx_kv_append(cfg: Config, cache, q, k, v, dtype, ldq, ldk, ldv, tokens, q_he
     """``cache``: an ``mx_kv_cache`` by reference."""
     return lib().mx_kv_append(cfg.ref(), cache, q, k, v, dtype, ldq, ldk, ldv, tokens, q_heads, q_gain, k_gain, eps,
                               inv_freq, rot_dim, interleaved, positions, slots, q_out, ldqo, k_out, ldko, stream)
+
+
+def mx_attn_decode(cfg: Config, cache, q, q_dtype, ldq, seqs, q_heads, page_table, ld_table, max_pages, lengths, scale,
+                   window, sinks, out, out_dtype, ldo, lse, workspace, workspace_bytes, stream) -> int:
+    """``cache``: an ``mx_kv_cache`` by reference."""
+    return lib().mx_attn_decode(cfg.ref(), cache, q, q_dtype, ldq, seqs, q_heads, page_table, ld_table, max_pages, lengths,
+                                scale, window, sinks, out, out_dtype, ldo, lse, workspace, workspace_bytes, stream)
 
 
 def mx_gemm_qsnr(ca: Config, cb: Config, A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB, stats,
@@ -716,6 +727,52 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
                           _ptr_or_none(k_out), ldko, st)
     _check("mx_kv_append", rc)
     return q_out, k_out
+
+
+def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, *,
+                scale: float | None = None, window: int = 0, sinks: int = 0, lse: bool = False,
+                out_dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None, stream=None):
+    """Attention of one query token per sequence, ``q`` ``[S, q_heads, head_dim]`` (or
+    ``[S, q_heads * head_dim]``), over the cache (``mx_attn_decode``).  ``page_table``: int32
+    ``[S, max_pages]``; ``lengths``: int32 ``[S]``, the query's own token included.  ``window`` > 0:
+    the last ``window`` tokens and the first ``sinks`` are visible.  ``scale``: 1 /
+    sqrt(head_dim) by default.  Returns ``[S, q_heads, head_dim]`` in q's dtype unless
+    ``out_dtype`` or ``out`` says otherwise, and with ``lse`` also the log sum exp, fp32
+    ``[S, q_heads]``.  Scratch is allocated per call unless ``workspace`` (uint8) is given."""
+    if not q.is_cuda:
+        raise ValueError("q must be a CUDA tensor")
+    D, dev, S = cache.head_dim, cache.device, q.shape[0]
+    if q.dtype not in _DT:
+        raise TypeError(f"unsupported dtype {q.dtype} (bf16 or fp32)")
+    _same_device(dev, q=q, page_table=page_table, out=out, workspace=workspace)
+    Hq = q.shape[1] if q.dim() == 3 else q.shape[1] // D
+    ldq = _heads(q, Hq, D, "q")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != S:
+        raise ValueError(f"page_table must be int32 [{S}, max_pages]")
+    pages = page_table.shape[1]
+    if (pages > 1 and page_table.stride(1) != 1) or (S > 1 and page_table.stride(0) < pages):
+        raise ValueError("page_table must have contiguous rows")
+    ldt = page_table.stride(0) if S > 1 else pages
+    pl = _vector(lengths, S, torch.int32, dev, "lengths")
+    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
+        raise ValueError("workspace must be contiguous uint8")
+    with _Launch(dev, stream) as st:
+        if out is None:
+            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=dev)
+        elif out.dtype not in _DT or out.shape[0] != S or out.dtype != (out_dtype or out.dtype):
+            raise ValueError(f"out must have {S} rows of {out_dtype or 'bf16 or fp32'}")
+        ldo = _heads(out, Hq, D, "out")
+        ref = cache.ref()
+        ls = torch.empty((S, Hq), dtype=torch.float32, device=dev) if lse else None
+        nbytes = lib().mx_attn_workspace_bytes(ref, S, Hq, pages, window, sinks)
+        if workspace is None and nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        rc = mx_attn_decode(cache.cfg, ref, q.data_ptr(), _DT[q.dtype], ldq, S, Hq, page_table.data_ptr(), ldt, pages, pl,
+                            D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _DT[out.dtype], ldo,
+                            _ptr_or_none(ls), _ptr_or_none(workspace), workspace.numel() if workspace is not None else 0, st)
+    _check("mx_attn_decode", rc)
+    return (out, ls) if lse else out
 
 
 def mbs_gemm_operand(q: Quantized, stream=None) -> Quantized:

@@ -8,6 +8,7 @@
 
 #include <new>
 
+#include "attn_kernel.cuh"
 #include "mma_decode.cuh"
 #include "mx.h"
 #include "mx_internal.h"
@@ -319,6 +320,13 @@ int check_cache(const mx_config *cfg, const mx_kv_cache *c)
     return MX_OK;
 }
 
+// the most tokens a sequence of a call can see
+int64_t attn_most(const mx_kv_cache *c, int64_t max_pages, int32_t window, int32_t sinks)
+{
+    const int64_t all = max_pages * c->page_size;
+    return window > 0 && (int64_t)window + sinks < all ? (int64_t)window + sinks : all;
+}
+
 }  // namespace
 
 extern "C" {
@@ -561,6 +569,85 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
     const float thr = cfg->rule == MX_RULE_CEIL ? p.ed.maxv : cfg->rule == MX_RULE_OAS ? cfg->oas_tau : INFINITY;
     p.thr_m = ldexpf(thr, -p.ed.emax);
     return launch_kv_append(p, cache->head_dim, dtype == MX_DT_FP32, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;
+}
+
+int64_t mx_attn_workspace_bytes(const mx_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_pages, int32_t window,
+                                int32_t sinks)
+{
+    if (!cache || seqs <= 0 || q_heads <= 0 || cache->kv_heads <= 0 || cache->page_size <= 0 || max_pages <= 0) return 0;
+    const int s = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks));
+    return s == 1 ? 0 : seqs * q_heads * s * (8 + 4 * (int64_t)cache->head_dim);
+}
+
+int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q, int32_t q_dtype, int64_t ldq,
+                   int64_t seqs, int32_t q_heads, const int32_t *page_table, int64_t ld_table, int64_t max_pages,
+                   const int32_t *lengths, float scale, int32_t window, int32_t sinks, void *out, int32_t out_dtype,
+                   int64_t ldo, float *lse, void *workspace, int64_t workspace_bytes, void *stream)
+{
+    const int rc = check_cache(cfg, cache);
+    if (rc != MX_OK) return rc;
+    if ((q_dtype != MX_DT_BF16 && q_dtype != MX_DT_FP32) || (out_dtype != MX_DT_BF16 && out_dtype != MX_DT_FP32))
+        return MX_ERR_INVALID;
+    if (seqs < 0 || seqs > (1 << 20) || q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads) return MX_ERR_INVALID;
+    if (max_pages < 0 || max_pages > INT32_MAX || max_pages * cache->page_size > INT32_MAX || window < 0 || sinks < 0)
+        return MX_ERR_INVALID;
+    if (!(scale > -INFINITY && scale < INFINITY)) return MX_ERR_INVALID;
+    if (seqs == 0) return MX_OK;
+    const int64_t cols = (int64_t)q_heads * cache->head_dim;
+    if (!q || !out || !lengths || (max_pages && !page_table)) return MX_ERR_INVALID;
+    if (ldq < cols || ldo < cols || (max_pages && ld_table < max_pages)) return MX_ERR_INVALID;
+    const int qs = q_dtype == MX_DT_FP32 ? 4 : 2, os = out_dtype == MX_DT_FP32 ? 4 : 2;
+    if ((uintptr_t)q % qs || (uintptr_t)out % os || (uintptr_t)page_table % 4 || (uintptr_t)lengths % 4 || (uintptr_t)lse % 4)
+        return MX_ERR_ALIGN;
+    const int splits = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks));
+    if (splits > 1) {
+        if (!workspace || workspace_bytes < mx_attn_workspace_bytes(cache, seqs, q_heads, max_pages, window, sinks))
+            return MX_ERR_WORKSPACE;
+        if (!aligned16(workspace)) return MX_ERR_ALIGN;
+    }
+
+    AttnParams p = {};
+    p.q = q;
+    p.ldq = ldq;
+    p.q_fp32 = q_dtype == MX_DT_FP32;
+    p.q_vec = aligned16(q) && (ldq * qs) % 16 == 0;
+    p.seqs = seqs;
+    p.q_heads = q_heads;
+    p.kv_heads = cache->kv_heads;
+    p.head_dim = cache->head_dim;
+    p.k_codes = static_cast<const uint8_t *>(cache->k_codes);
+    p.v_codes = static_cast<const uint8_t *>(cache->v_codes);
+    p.k_scales = cache->k_scales;
+    p.v_scales = cache->v_scales;
+    p.scale_bytes = cache->pages * cache->page_size * cache->kv_heads * (cache->head_dim / cfg->block);
+    p.k_ts = cfg->tensor_scale != MX_TS_NONE ? cache->k_tensor_scale : nullptr;
+    p.v_ts = cfg->tensor_scale != MX_TS_NONE ? cache->v_tensor_scale : nullptr;
+    p.sfmt = cfg->scale_fmt;
+    while ((1 << p.log2B) < cfg->block) ++p.log2B;
+    p.pages = (int)cache->pages;
+    p.page_size = cache->page_size;
+    p.page_shift = -1;
+    if (is_pow2(cache->page_size)) {
+        p.page_shift = 0;
+        while ((1 << p.page_shift) < cache->page_size) ++p.page_shift;
+    }
+    p.table = page_table;
+    p.ld_table = ld_table;
+    p.max_pages = (int)max_pages;
+    p.lengths = lengths;
+    p.scale = scale;
+    p.window = window;
+    p.sinks = sinks;
+    p.out = out;
+    p.ldo = ldo;
+    p.o_fp32 = out_dtype == MX_DT_FP32;
+    p.lse = lse;
+    p.splits = splits;
+    p.part_o = static_cast<float *>(workspace);
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + (splits > 1 ? seqs * q_heads * splits * cache->head_dim : 0));
+    const int el = cfg->elem == MX_E2M1 ? GE_E2M1 : cfg->elem == MX_E3M0 ? GE_E3M0 : cfg->elem == MX_INT4 ? GE_INT4
+                 : cfg->elem == MX_E2M3 ? AE_E2M3 : AE_E3M2;
+    return launch_attn(p, el, p.q_fp32 || p.o_fp32, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;
 }
 
 int mx_tensor_amax(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t rows, int64_t cols,

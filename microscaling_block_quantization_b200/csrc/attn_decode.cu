@@ -1,0 +1,112 @@
+// mx_attn_decode's launches: the kernel of the cache's format, the split of
+// the sequences, and the join of the partial results.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "attn_kernel.cuh"
+
+namespace mxk {
+
+namespace {
+
+constexpr int kJoinThreads = 256;
+
+// One CTA per (sequence, query head): the splits' sums brought to the common
+// maximum and added in order.  Each of the CTA's groups of D threads takes
+// every (256 / D)-th split; the groups' sums meet in shared memory.
+__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnParams p)
+{
+    __shared__ float red[kJoinThreads];
+    __shared__ float wl[kJoinThreads / 32][2];
+    const int D = p.head_dim, groups = kJoinThreads / D, d = threadIdx.x % D, grp = threadIdx.x / D;
+    const int64_t out = blockIdx.x;                     // sequence * q_heads + head
+    const int seq = (int)(out / p.q_heads), head = (int)(out % p.q_heads);
+    pdl_trigger();
+    pdl_wait();
+    int n, vis, sinks;
+    at_visible(p, seq, n, vis, sinks);
+    const int tiles = (vis + 15) >> 4, per = (tiles + p.splits - 1) / p.splits;
+    const int used = per ? (tiles + per - 1) / per : 0;
+    const float2 *ml = p.part_ml + out * p.splits;
+    float m = -INFINITY;
+    for (int s = threadIdx.x; s < used; s += kJoinThreads) m = fmaxf(m, ml[s].x);
+#pragma unroll
+    for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    if ((threadIdx.x & 31) == 0) wl[threadIdx.x >> 5][0] = m;
+    __syncthreads();
+    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, wl[i][0]);
+    float l = 0.0f, o = 0.0f;
+#pragma unroll 4
+    for (int s = grp; s < used; s += groups) {
+        const float2 x = ml[s];
+        // a stretch without a visible token has m = -inf, l = 0; one whose
+        // scores are NaN makes the result NaN
+        const float w = x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : exp2f(x.x - m);
+        l = fmaf(w, x.y, l);
+        o = fmaf(w, p.part_o[(out * p.splits + s) * D + d], o);
+    }
+    red[threadIdx.x] = o;
+    __syncthreads();
+    if (grp == 0)
+        for (int i = 1; i < groups; ++i) o += red[i * D + d];
+    __syncthreads();
+    red[threadIdx.x] = l;
+    __syncthreads();
+    if (grp) return;
+    for (int i = 1; i < groups; ++i) l += red[i * D + d];
+    const bool any = l > 0.0f || l != l;
+    const float v = any ? __fdiv_rn(o, l) : 0.0f;
+    const int64_t at = (int64_t)seq * p.ldo + (int64_t)head * D + d;
+    if (p.o_fp32) static_cast<float *>(p.out)[at] = v;
+    else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+    if (d == 0 && p.lse) p.lse[out] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
+}
+
+AtPick at_pick(int el, int d, int bs, int nth, int hp)
+{
+#define AT_CASE(EL) \
+    case EL: return d == 64 ? at_kernel_##EL##_64(bs, nth, hp) : d == 128 ? at_kernel_##EL##_128(bs, nth, hp) : at_kernel_##EL##_256(bs, nth, hp);
+    switch (el) {
+        AT_CASE(GE_E2M1)
+        AT_CASE(GE_E3M0)
+        AT_CASE(GE_INT4)
+        AT_CASE(AE_E2M3)
+    default: return d == 64 ? at_kernel_AE_E3M2_64(bs, nth, hp) : d == 128 ? at_kernel_AE_E3M2_128(bs, nth, hp) : at_kernel_AE_E3M2_256(bs, nth, hp);
+    }
+#undef AT_CASE
+}
+
+}  // namespace
+
+// Splits of every sequence for a call of these sizes: enough warps to fill
+// the device about twice (ragged sequences even out), stretches of 128 tokens
+// at least.
+int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens)
+{
+    const int group = q_heads / kv_heads;
+    const int hg = group <= 4 ? 1 : (group + 7) / 8;
+    const int64_t rows = seqs * kv_heads * hg;
+    if (rows <= 0) return 1;
+    const int64_t want = (int64_t)device_sm_count() * 32;
+    int64_t s = want / rows;
+    const int64_t cap = (most_tokens + 127) / 128;
+    s = s < cap ? s : cap;
+    return s < 1 ? 1 : s > kAttnMaxSplits ? kAttnMaxSplits : (int)s;
+}
+
+int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
+{
+    p.group = p.q_heads / p.kv_heads;
+    const int nth = p.group <= 4 ? 1 : 2;
+    p.head_groups = (p.group + 4 * nth - 1) / (4 * nth);
+    p.tasks = p.seqs * p.splits * p.head_groups * p.kv_heads;
+    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : 32, nth, hp);
+    if (k.smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(k.k), k.smem)) return 1;
+    const int64_t ctas = (p.tasks + kAtWarps - 1) / kAtWarps;
+    if (launch_pdl(k.k, (unsigned)ctas, kAtThreads, k.smem, st, p) != cudaSuccess) return 1;
+    if (p.splits == 1) return 0;
+    return launch_pdl(k_attn_join, (unsigned)(p.seqs * p.q_heads), kJoinThreads, 0, st, p) == cudaSuccess ? 0 : 1;
+}
+
+}  // namespace mxk

@@ -1,0 +1,8 @@
+// mx_attn_decode kernels of INT4 caches, heads of 64.
+#include "attn_kernel.cuh"
+
+namespace mxk {
+
+AT_DEFINE(GE_INT4, 64)
+
+}  // namespace mxk

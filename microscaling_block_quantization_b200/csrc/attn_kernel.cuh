@@ -1,0 +1,635 @@
+// Attention of one query token per sequence over a paged block-scaled cache
+// (mx_attn_decode).
+//
+//   o_h = sum_t p_t v_t / sum_t p_t,  p_t = exp(scale q_h . k_t - m_h),  t over the visible tokens;
+//   k_t, v_t = q s_b (s_T) of the cache's codes.
+//
+// Bound: the visible rows' codes and scales read once for all query heads of
+// a key head.  Per key element a group of G heads takes 2 G multiply-adds, so
+// the products run on the matrix instruction, and the work per byte is the
+// codes' conversion to f16.
+//
+// A warp takes a (sequence, key head, eight query heads, stretch of tokens)
+// and walks it 16 tokens at a time, rows fetched through the page table by
+// asynchronous copies into a private ring; warps do not wait for one another.
+// Consecutive warps take consecutive key heads, whose rows are contiguous.
+//
+// * Scores: 16 tokens x 8 heads, codes as the 16-row operand, queries as f16
+//   pieces scaled by a power of two per head (bf16: one piece exact down to
+//   2^-31 of the head's largest; binary32: two, exact); each block's sum times
+//   its scale in binary32.
+// * One pass with a running maximum m (reference for the exponentials) and
+//   sum l per head in binary32.  m moves only when a score exceeds it by 4
+//   (in powers of two), so most tiles rescale nothing.
+// * p v: tokens are the reduction dimension, but a decoded code pair holds
+//   neighbours along the head.  The reduction index is (token, parity), the
+//   eight columns (head, parity), and the weight of column (h, r) at (t, e) is
+//   p_t(h) where e = r, else 0: code pairs enter the instruction as decoded,
+//   nothing is transposed, and each m16 tile is one 32-block of the head, so
+//   that the block's scale multiplies the weight: w = p s_b, in binary32.
+// * w as f16: scaled by 2^7 and, per 32-block, by a reference exponent of the
+//   block scales that also moves rarely, so w stays in [0, 2^15]; a weight is
+//   flushed only below 2^-32 of its block's largest.  One f16 rounding
+//   (2^-11) per weight for bf16 results; for binary32 a second piece holds
+//   the rounding's remainder (2^-22).
+// * Partial results (unnormalised sums, m, l) of a sequence's stretches meet
+//   in a second launch, in order.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "mma_decode.cuh"
+#include "mx_internal.h"
+
+namespace mxk {
+
+// element kinds: the 4-bit ones of GE_*, then one code per byte
+enum { AE_E2M3 = 4, AE_E3M2 = 5 };
+
+constexpr int kAtWarps = 4;
+constexpr int kAtThreads = kAtWarps * 32;
+
+template <int EL, int D, int BS> struct AtGeom {
+    static constexpr int BITS = EL >= AE_E2M3 ? 8 : 4;
+    static constexpr int NB = D / 32;                  // 32-blocks of a head
+    static constexpr int ROW = D * BITS / 8;           // bytes of a head's codes
+    static constexpr int NPC = ROW / 16;               // 16-byte pieces
+    // bytes kept of a token's scales: all of them (blocks of 16), a word at least
+    static constexpr int SW = BS == 16 ? D / 16 : (D / 32 < 4 ? 4 : D / 32);
+    static constexpr int K_AT = 0, V_AT = 16 * ROW, KS_AT = 32 * ROW, VS_AT = KS_AT + 16 * SW, META_AT = VS_AT + 16 * SW;
+    static constexpr int STAGE = META_AT + 16;
+    static constexpr int STAGES = STAGE * 4 * kAtWarps <= 48 * 1024 ? 4 : 3;
+    // piece swizzle by row: the eight rows a K read touches at once, and the
+    // four of a V read, fall on different banks
+    static __host__ __device__ constexpr int swz(int row)
+    {
+        return BITS == 8 && NPC == 4 ? (row & 2) | ((row >> 2) & 1) : BITS == 8 ? ((row & 3) << 1) | ((row >> 2) & 1)
+               : NPC == 2 ? (row >> 2) & 1 : NPC == 4 ? (row >> 1) & 3 : row & 7;
+    }
+};
+
+__device__ __forceinline__ void cp_async_n(uint32_t dst, const void *src, int n, int src_bytes)
+{
+    if (n == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+    else if (n == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a)
+{
+    uint2 r;
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+// two codes (a byte of 4-bit codes, or 16 bits of FP6) -> f16x2
+template <int EL> __device__ __forceinline__ uint32_t pair_half2(uint32_t c)
+{
+    uint32_t r;
+    if (EL == GE_E2M1) {
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(r) : "r"(c));
+    } else if (EL == AE_E2M3) {
+        asm("cvt.rn.f16x2.e2m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+    } else if (EL == AE_E3M2) {
+        asm("cvt.rn.f16x2.e3m2x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
+    } else {
+        uint32_t h[4];
+        codes8_halves<EL>(c & 0xffu, h);
+        r = h[0];
+    }
+    return r;
+}
+
+// Eight codes of lane t in 32-block b of a key row -> four f16x2.
+template <int EL, int D, int BS>
+__device__ __forceinline__ void at_key_codes(uint32_t kt, int row, int b, int t, uint32_t h[4])
+{
+    using G = AtGeom<EL, D, BS>;
+    const int z = G::swz(row);
+    if constexpr (G::BITS == 4) {
+        const uint32_t p = kt + row * G::ROW + ((b ^ z) << 4);
+        uint32_t w;
+        if (BS == 16) w = __byte_perm(lds32(p + 4 * (t >> 1)), lds32(p + 8 + 4 * (t >> 1)), (t & 1) ? 0x7632u : 0x5410u);
+        else w = lds32(p + 4 * t);
+        codes8_halves<EL>(w, h);
+    } else {
+        // blocks of 16: four codes of each half of the 32-block
+        uint2 w;
+        if (BS == 16) {
+            w.x = lds32(kt + row * G::ROW + (((2 * b) ^ z) << 4) + 4 * t);
+            w.y = lds32(kt + row * G::ROW + (((2 * b + 1) ^ z) << 4) + 4 * t);
+        } else {
+            w = lds64(kt + row * G::ROW + (((2 * b + (t >> 1)) ^ z) << 4) + 8 * (t & 1));
+        }
+        h[0] = pair_half2<EL>(w.x);
+        h[1] = pair_half2<EL>(w.x >> 16);
+        h[2] = pair_half2<EL>(w.y);
+        h[3] = pair_half2<EL>(w.y >> 16);
+    }
+}
+
+// Code pairs 2g, 2g + 1 (blocks of 16: g and g + 8) of 32-block b of a value
+// row -> the operand's rows g and g + 8.
+template <int EL, int D, int BS>
+__device__ __forceinline__ void at_value_codes(uint32_t vt, int row, int b, int g, uint32_t &lo, uint32_t &hi)
+{
+    using G = AtGeom<EL, D, BS>;
+    const int z = G::swz(row);
+    const uint32_t r = vt + row * G::ROW;
+    if constexpr (G::BITS == 4) {
+        const uint32_t p = r + ((b ^ z) << 4);
+        if (BS == 16) {
+            lo = pair_half2<EL>(lds16(p + (g & 6)) >> (8 * (g & 1)));
+            hi = pair_half2<EL>(lds16(p + 8 + (g & 6)) >> (8 * (g & 1)));
+        } else {
+            const uint32_t w = lds16(p + 2 * g);
+            lo = pair_half2<EL>(w);
+            hi = pair_half2<EL>(w >> 8);
+        }
+    } else if (BS == 16) {
+        lo = pair_half2<EL>(lds16(r + (((2 * b) ^ z) << 4) + 2 * g));
+        hi = pair_half2<EL>(lds16(r + (((2 * b + 1) ^ z) << 4) + 2 * g));
+    } else {
+        const uint32_t w = lds32(r + (((2 * b + (g >> 2)) ^ z) << 4) + 4 * (g & 3));
+        lo = pair_half2<EL>(w);
+        hi = pair_half2<EL>(w >> 16);
+    }
+}
+
+// A token's scales -> binary32, one per 32-block (two with blocks of 16).
+template <int EL, int D, int BS>
+__device__ __forceinline__ void at_scales(const AttnParams &p, uint32_t area, int tok, uint32_t shifts, const uint32_t sel[2],
+                                          float *s)
+{
+    using G = AtGeom<EL, D, BS>;
+    const uint32_t a = area + tok * G::SW;
+    if (BS == 16) {
+#pragma unroll
+        for (int i = 0; i < G::SW / 4; ++i) scales4(p.sfmt, lds32(a + 4 * i), s + 4 * i);
+        return;
+    }
+    uint32_t w0 = lds32(a) >> shifts, w1 = 0u;
+    if (G::SW > 4) w1 = lds32(a + 4);
+    float f[4];
+    scales4(p.sfmt, __byte_perm(w0, w1, sel[0]), f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        if (i < G::NB) s[i] = f[i];
+    if (G::NB > 4) {
+        scales4(p.sfmt, __byte_perm(w0, w1, sel[1]), f);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (4 + i < G::NB) s[4 + i] = f[i];
+    }
+}
+
+// Eight consecutive query values.
+__device__ __forceinline__ void at_load8(const AttnParams &p, int64_t at, bool on, float v[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    if (!on) return;
+    if (p.q_fp32) {
+        const float *x = static_cast<const float *>(p.q) + at;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = x[i];
+    } else {
+        const uint16_t *x = static_cast<const uint16_t *>(p.q) + at;
+        if (p.q_vec) {
+            const uint4 a = *reinterpret_cast<const uint4 *>(x);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[2 * i] = bits2f(w[i] << 16);
+                v[2 * i + 1] = bits2f(w[i] & 0xffff0000u);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = bits2f((uint32_t)x[i] << 16);
+        }
+    }
+}
+
+// visible tokens of a sequence, and the token of visible index i
+__device__ __forceinline__ void at_visible(const AttnParams &p, int b, int &n, int &vis, int &sinks)
+{
+    n = max(p.lengths[b], 0);
+    n = (int)min((int64_t)n, (int64_t)p.max_pages * p.page_size);
+    sinks = 0;
+    vis = n;
+    if (p.window > 0) {
+        const int first = max(n - p.window, 0);      // the window's first token
+        sinks = min(p.sinks, first);
+        vis = n - first + sinks;
+    }
+}
+
+// NTH: groups of four heads (1 or 2); HP: binary32 precision (two pieces of
+// queries and weights)
+template <int EL, int D, int BS, int NTH, int HP>
+__global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ AttnParams p)
+{
+    using G = AtGeom<EL, D, BS>;
+    constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int g = lane >> 2, t = lane & 3;
+    pdl_trigger();
+    pdl_wait();
+
+    // the warp's task: key head fastest, then head group, split, sequence
+    int64_t task = (int64_t)blockIdx.x * kAtWarps + warp;
+    if (task >= p.tasks) return;
+    const int kh = (int)(task % p.kv_heads);
+    task /= p.kv_heads;
+    const int hg = (int)(task % p.head_groups);
+    task /= p.head_groups;
+    const int split = (int)(task % p.splits), seq = (int)(task / p.splits);
+    const int h0 = kh * p.group + hg * (4 * NTH);           // first query head
+    const int hn = min(4 * NTH, p.group - hg * (4 * NTH));  // heads of this task
+    int n, vis, sinks;
+    at_visible(p, seq, n, vis, sinks);
+    const int tiles = (vis + 15) >> 4, per = (tiles + p.splits - 1) / p.splits;
+    const int tile0 = split * per, tile1 = min(tile0 + per, tiles);
+    if (tile0 >= tile1 && p.splits > 1) return;   // (the join reads no more than the splits in use)
+
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::STAGES * G::STAGE;
+    const int skip = n - vis;                 // tokens between the sinks and the window
+    const int32_t *table = p.table + (int64_t)seq * p.ld_table;
+    const int nsc = D >> p.log2B;             // scales of a head
+    const int64_t code_row = (int64_t)p.kv_heads * G::ROW, sc_row = (int64_t)p.kv_heads * nsc;
+    const uint8_t *kc = p.k_codes + kh * G::ROW, *vc = p.v_codes + kh * G::ROW;
+    // lanes 0..15 copy key scales of their token, 16..31 value scales
+    const uint8_t *sc = lane < 16 ? p.k_scales : p.v_scales;
+
+    // page number of the lane's token (lane & 15) in a tile; -1 behind the end
+    auto page_of = [&](int tile, int &off) {
+        const int i = tile * 16 + (lane & 15);
+        if (tile >= tile1 || i >= vis) return -1;
+        const int tok = i < sinks ? i : i + skip;
+        const int pg = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
+        off = tok - pg * p.page_size;
+        return (int)table[pg];
+    };
+    int next_off = 0, next_page = page_of(tile0, next_off), it = tile0;
+    uint32_t st_w = ring;
+    auto issue = [&]() {
+        if (it < tile1) {
+            const bool ok = next_page >= 0 && next_page < p.pages;
+            const int row = ok ? next_page * p.page_size + next_off : -1;
+            ++it;
+            next_page = page_of(it, next_off);
+#pragma unroll
+            for (int i = 0; i < G::NPC / 2; ++i) {
+                const int idx = i * 32 + lane, r = idx / G::NPC, pc = idx % G::NPC;
+                const int src = __shfl_sync(0xffffffffu, row, r);
+                const int64_t at = src < 0 ? 0 : (int64_t)src * code_row + pc * 16;
+                const uint32_t dst = st_w + r * G::ROW + ((pc ^ G::swz(r)) << 4);
+                cp_async16(dst + G::K_AT, kc + at, src < 0 ? 0 : 16);
+                cp_async16(dst + G::V_AT, vc + at, src < 0 ? 0 : 16);
+            }
+            int shift = 0;
+            {
+                const int64_t at = row < 0 ? 0 : (int64_t)row * sc_row + kh * nsc;
+                const uint32_t dst = st_w + (lane < 16 ? G::KS_AT : G::VS_AT) + (lane & 15) * G::SW;
+                if (nsc >= 4) {
+                    cp_async_n(dst, sc + at, nsc, row < 0 ? 0 : nsc);
+                } else {
+                    // one or two bytes: the aligned word around them
+                    shift = (int)(at & 3);
+                    const int64_t w = at & ~(int64_t)3;
+                    cp_async_n(dst, sc + w, 4, row < 0 ? 0 : (int)min((int64_t)4, p.scale_bytes - w));
+                }
+            }
+            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
+            const uint32_t b0 = __ballot_sync(0xffffffffu, shift & 1), b1 = __ballot_sync(0xffffffffu, shift & 2);
+            if (lane == 0)
+                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(st_w + G::META_AT), "r"(mask & 0xffffu), "r"(b0 & 0xffffu),
+                             "r"(b1 & 0xffffu), "r"(0u) : "memory");
+        }
+        st_w = st_w + G::STAGE == ring + G::STAGES * G::STAGE ? ring : st_w + G::STAGE;
+        cp_async_commit();
+    };
+#pragma unroll
+    for (int i = 0; i < G::STAGES - 1; ++i) issue();
+
+    // queries: lane (g, t) holds head h0 + g at the k places of its code words
+    uint32_t qf[PC][NB][4];
+    float qe;                                 // 2^-e of head h0 + g
+    {
+        float v[NB][8];
+        uint32_t m = 0;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            const int64_t at = (int64_t)seq * p.ldq + (int64_t)(h0 + g) * D + 32 * b;
+            if (BS == 16) {
+                // codes 4t.. of the first half, 4t.. of the second
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int64_t e = at + 16 * (i >> 2) + 4 * t + (i & 3);
+                    v[b][i] = g >= hn ? 0.0f : p.q_fp32 ? static_cast<const float *>(p.q)[e]
+                                                        : bits2f((uint32_t)static_cast<const uint16_t *>(p.q)[e] << 16);
+                }
+            } else {
+                at_load8(p, at + 8 * t, g < hn, v[b]);
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[b][i]) & 0x7fffffffu);
+        }
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const int e = f16_scale_exponent(bits2f(m));
+        const float f = exp2i(e);
+        qe = exp2i(-e);
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float x = __fmul_rn(v[b][2 * i], f), y = __fmul_rn(v[b][2 * i + 1], f);
+                const __half2 h = __floats2half2_rn(x, y);
+                qf[0][b][i] = *reinterpret_cast<const uint32_t *>(&h);
+                if (HP) {
+                    const float2 back = __half22float2(h);
+                    float rx = __fmul_rn(__fsub_rn(x, back.x), 2048.0f), ry = __fmul_rn(__fsub_rn(y, back.y), 2048.0f);
+                    rx = rx == rx ? rx : 0.0f;
+                    ry = ry == ry ? ry : 0.0f;
+                    const __half2 h2 = __floats2half2_rn(rx, ry);
+                    qf[PC - 1][b][i] = *reinterpret_cast<const uint32_t *>(&h2);
+                }
+            }
+    }
+    // score factor of heads 2t and 2t + 1: softmax scale, log2 e, tensor scale
+    const float base = p.scale * 1.44269504088896340736f;
+    const float kts = p.k_ts ? *p.k_ts : 1.0f;
+    const float fac0 = __fmul_rn(__fmul_rn(base, kts), __shfl_sync(0xffffffffu, qe, 8 * t));
+    const float fac1 = __fmul_rn(__fmul_rn(base, kts), __shfl_sync(0xffffffffu, qe, 8 * t + 4));
+    // scale bytes of the 32-blocks within the token's words
+    uint32_t sel[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sel[i >> 2] |= (uint32_t)((32 * i) >> p.log2B) << (4 * (i & 3));
+
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.0f, l1 = 0.0f;   // heads 2t, 2t + 1
+    float cb[NB];                             // 2^-E of the value blocks' reference exponents
+    float acc[NTH][NB][4];
+#pragma unroll
+    for (int j = 0; j < NB; ++j) {
+        cb[j] = 0.0f;                         // (none yet)
+#pragma unroll
+        for (int q = 0; q < NTH; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[q][j][i] = 0.0f;
+    }
+
+    uint32_t st = ring;
+    for (int tile = tile0; tile < tile1; ++tile) {
+        cp_async_wait<G::STAGES - 2>();
+        __syncwarp();                         // the tile is in, and the last one is read
+        issue();
+        const uint4 meta = lds128(st + G::META_AT);
+
+        // scores of tokens g, g + 8 (heads 2t, 2t + 1)
+        float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        {
+            float kl[NB * SUB], kg[NB * SUB];
+            const int sl = (((meta.y >> g) & 1) | (((meta.z >> g) & 1) << 1)) * 8;
+            const int sh = (((meta.y >> (g + 8)) & 1) | (((meta.z >> (g + 8)) & 1) << 1)) * 8;
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g, sl, sel, kl);
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, sh, sel, kg);
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                uint32_t lo[4], hi[4];
+                at_key_codes<EL, D, BS>(st + G::K_AT, g, b, t, lo);
+                at_key_codes<EL, D, BS>(st + G::K_AT, g + 8, b, t, hi);
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    float d[4], e[4];
+                    if (SUB == 2) {
+                        mma_16816_zero(d, lo[2 * u], hi[2 * u], lo[2 * u + 1], hi[2 * u + 1], qf[0][b][2 * u], qf[0][b][2 * u + 1]);
+                        if (HP) mma_16816_zero(e, lo[2 * u], hi[2 * u], lo[2 * u + 1], hi[2 * u + 1], qf[PC - 1][b][2 * u], qf[PC - 1][b][2 * u + 1]);
+                    } else {
+                        mma_16816_zero(d, lo[0], hi[0], lo[1], hi[1], qf[0][b][0], qf[0][b][1]);
+                        mma_16816(d, lo[2], hi[2], lo[3], hi[3], qf[0][b][2], qf[0][b][3]);
+                        if (HP) {
+                            mma_16816_zero(e, lo[0], hi[0], lo[1], hi[1], qf[PC - 1][b][0], qf[PC - 1][b][1]);
+                            mma_16816(e, lo[2], hi[2], lo[3], hi[3], qf[PC - 1][b][2], qf[PC - 1][b][3]);
+                        }
+                    }
+                    if (HP) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) d[i] = fmaf(e[i], 0x1p-11f, d[i]);
+                    }
+                    s[0] = fmaf(kl[b * SUB + u], d[0], s[0]);
+                    s[1] = fmaf(kl[b * SUB + u], d[1], s[1]);
+                    s[2] = fmaf(kg[b * SUB + u], d[2], s[2]);
+                    s[3] = fmaf(kg[b * SUB + u], d[3], s[3]);
+                }
+            }
+        }
+        const bool on_l = (meta.x >> g) & 1, on_h = (meta.x >> (g + 8)) & 1;
+        s[0] = on_l ? __fmul_rn(s[0], fac0) : -INFINITY;
+        s[1] = on_l ? __fmul_rn(s[1], fac1) : -INFINITY;
+        s[2] = on_h ? __fmul_rn(s[2], fac0) : -INFINITY;
+        s[3] = on_h ? __fmul_rn(s[3], fac1) : -INFINITY;
+
+        // move the reference when a score passes it by 2^4
+        if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m0 + 4.0f || fmaxf(s[1], s[3]) > m1 + 4.0f)) {
+            float a = fmaxf(m0, fmaxf(s[0], s[2])), c = fmaxf(m1, fmaxf(s[1], s[3]));
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
+                c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
+            }
+            const float r0 = m0 == a ? 1.0f : exp2f(m0 - a), r1 = m1 == c ? 1.0f : exp2f(m1 - c);
+            m0 = a;
+            m1 = c;
+            l0 *= r0;
+            l1 *= r1;
+            // the sums of head t (+ 4): its factor is with lane t >> 1 (+ 2)
+#pragma unroll
+            for (int q = 0; q < NTH; ++q) {
+                const float x = __shfl_sync(0xffffffffu, r0, (t >> 1) + 2 * q), y = __shfl_sync(0xffffffffu, r1, (t >> 1) + 2 * q);
+                const float r = (t & 1) ? y : x;
+#pragma unroll
+                for (int j = 0; j < NB; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
+            }
+        }
+        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+        s[0] = exp2f(s[0] - b0);
+        s[1] = exp2f(s[1] - b1);
+        s[2] = exp2f(s[2] - b0);
+        s[3] = exp2f(s[3] - b1);
+        l0 += s[0] + s[2];
+        l1 += s[1] + s[3];
+
+        // value scales of tokens t, t + 4, t + 8, t + 12
+        float vs[4][NB * SUB];
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int tk = t + 4 * i;
+            at_scales<EL, D, BS>(p, st + G::VS_AT, tk, (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8, sel, vs[i]);
+#pragma unroll
+            for (int j = 0; j < NB * SUB; ++j) top = fmaxf(top, __fmul_rn(vs[i][j], cb[j / SUB]));
+        }
+        // new reference exponents when a scale passes its own by 2^3, or at first
+        if (__any_sync(0xffffffffu, top > 8.0f || cb[0] == 0.0f)) {
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                float x = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) x = fmaxf(x, vs[i][j * SUB + u]);
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                // 2^-floor(log2 x), within 2^-100 .. 2^100
+                const int e = min(max((int)(__float_as_uint(x) >> 23) - 127, -100), 100);
+                const float c = exp2i(-e);
+                if (cb[j] == 0.0f || c < cb[j]) {
+                    const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
+#pragma unroll
+                    for (int q = 0; q < NTH; ++q)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
+                    cb[j] = c;
+                }
+            }
+        }
+        // weights p of the lane's tokens and column head, times 2^7
+        float pw[NTH][4];
+#pragma unroll
+        for (int q = 0; q < NTH; ++q) {
+            const int src = (g >> 2) + 2 * q;       // lane part of head (g >> 1) + 4 q
+            const bool odd = (g >> 1) & 1;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float x0 = __shfl_sync(0xffffffffu, s[0], (t + 4 * i) * 4 + src), x1 = __shfl_sync(0xffffffffu, s[1], (t + 4 * i) * 4 + src);
+                const float y0 = __shfl_sync(0xffffffffu, s[2], (t + 4 * i) * 4 + src), y1 = __shfl_sync(0xffffffffu, s[3], (t + 4 * i) * 4 + src);
+                pw[q][i] = __fmul_rn(odd ? x1 : x0, 128.0f);
+                pw[q][2 + i] = __fmul_rn(odd ? y1 : y0, 128.0f);
+            }
+        }
+        const int par = (g & 1) * 16;               // the column's parity
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) at_value_codes<EL, D, BS>(st + G::V_AT, t + 4 * i, j, g, lo[i], hi[i]);
+#pragma unroll
+            for (int q = 0; q < NTH; ++q)
+#pragma unroll
+                for (int u = 0; u < SUB; ++u) {
+                    uint32_t w[PC][4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = __fmul_rn(__fmul_rn(pw[q][i], cb[j]), vs[i][j * SUB + u]);
+                        const __half h = __float2half_rn(x);
+                        w[0][i] = (uint32_t)__half_as_ushort(h) << par;
+                        if (HP) w[PC - 1][i] = (uint32_t)__half_as_ushort(__float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(h)), 2048.0f))) << par;
+                    }
+                    // blocks of 16: rows below 8 are the first half's pairs,
+                    // the others the second's, each against its own weights
+                    const uint32_t z = 0u;
+#define AT_PV(d, wt)                                                                                                          \
+    if (SUB == 1) {                                                                                                           \
+        mma_16816(d, lo[0], hi[0], lo[1], hi[1], wt[0], wt[1]);                                                               \
+        mma_16816(d, lo[2], hi[2], lo[3], hi[3], wt[2], wt[3]);                                                               \
+    } else if (u == 0) {                                                                                                      \
+        mma_16816(d, lo[0], z, lo[1], z, wt[0], wt[1]);                                                                       \
+        mma_16816(d, lo[2], z, lo[3], z, wt[2], wt[3]);                                                                       \
+    } else {                                                                                                                  \
+        mma_16816(d, z, hi[0], z, hi[1], wt[0], wt[1]);                                                                       \
+        mma_16816(d, z, hi[2], z, hi[3], wt[2], wt[3]);                                                                       \
+    }
+                    AT_PV(acc[q][j], w[0])
+                    if (HP) {
+                        float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        AT_PV(e, w[PC - 1])
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[q][j][i] = fmaf(e[i], 0x1p-11f, acc[q][j][i]);
+                    }
+#undef AT_PV
+                }
+        }
+        st = st + G::STAGE == ring + G::STAGES * G::STAGE ? ring : st + G::STAGE;
+    }
+    cp_async_wait<0>();
+
+    // the sums over the lanes that share heads
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1) {
+        l0 += __shfl_xor_sync(0xffffffffu, l0, d);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, d);
+    }
+    const float vts = p.v_ts ? *p.v_ts : 1.0f;
+#pragma unroll
+    for (int q = 0; q < NTH; ++q) {
+        const int src = (t >> 1) + 2 * q, head = t + 4 * q;
+        const float ma = __shfl_sync(0xffffffffu, m0, src), mb = __shfl_sync(0xffffffffu, m1, src);
+        const float la = __shfl_sync(0xffffffffu, l0, src), lb = __shfl_sync(0xffffffffu, l1, src);
+        const float m = (t & 1) ? mb : ma, l = (t & 1) ? lb : la;
+        if (head >= hn) continue;
+        const int64_t out = (int64_t)seq * p.q_heads + h0 + head;
+        const bool whole = p.splits == 1;
+        // of no tokens: zeros; else over the sum (a join divides later)
+        const float div = !whole ? 1.0f : l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+        if (g == 0) {
+            if (!whole) p.part_ml[out * p.splits + split] = make_float2(m, l);
+            else if (p.lse) p.lse[out] = l > 0.0f || l != l ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            // 2^(E - 7) of the block, the tensor scale, the sum
+            const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - 7 - (int)(__float_as_uint(cb[j]) >> 23)), vts);
+            float o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = div == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(acc[q][j][i], f), div);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int d = 32 * j + (BS == 16 ? 2 * g + 16 * i : 4 * g + 2 * i);
+                if (!whole) {
+                    *reinterpret_cast<float2 *>(p.part_o + (out * p.splits + split) * D + d) = make_float2(o[2 * i], o[2 * i + 1]);
+                } else {
+                    const int64_t at = (int64_t)seq * p.ldo + (int64_t)(h0 + head) * D + d;
+                    if (p.o_fp32) {
+                        static_cast<float *>(p.out)[at] = o[2 * i];
+                        static_cast<float *>(p.out)[at + 1] = o[2 * i + 1];
+                    } else {
+                        static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(o[2 * i]);
+                        static_cast<__nv_bfloat16 *>(p.out)[at + 1] = __float2bfloat16_rn(o[2 * i + 1]);
+                    }
+                }
+            }
+        }
+    }
+}
+
+typedef void (*AtKernel)(const AttnParams);
+struct AtPick { AtKernel k; int smem; };
+
+template <int EL, int D, int BS> AtPick at_pick_nth(int nth, int hp)
+{
+    const int smem = kAtWarps * AtGeom<EL, D, BS>::STAGES * AtGeom<EL, D, BS>::STAGE;
+    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1> : k_attn<EL, D, BS, 1, 0>, smem};
+    return {hp ? k_attn<EL, D, BS, 2, 1> : k_attn<EL, D, BS, 2, 0>, smem};
+}
+template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp)
+{
+    return bs == 16 ? at_pick_nth<EL, D, 16>(nth, hp) : at_pick_nth<EL, D, 32>(nth, hp);
+}
+
+// the kernels of one element kind and head length, in translation units of their own
+#define AT_DECLARE(EL, D) AtPick at_kernel_##EL##_##D(int bs, int nth, int hp);
+#define AT_DECLARE3(EL) AT_DECLARE(EL, 64) AT_DECLARE(EL, 128) AT_DECLARE(EL, 256)
+AT_DECLARE3(GE_E2M1)
+AT_DECLARE3(GE_E3M0)
+AT_DECLARE3(GE_INT4)
+AT_DECLARE3(AE_E2M3)
+AT_DECLARE3(AE_E3M2)
+#undef AT_DECLARE3
+#undef AT_DECLARE
+#define AT_DEFINE(EL, D) \
+    AtPick at_kernel_##EL##_##D(int bs, int nth, int hp) { return at_pick_bs<EL, D>(bs, nth, hp); }
+
+}  // namespace mxk

@@ -122,6 +122,38 @@ struct KvAppendParams {
     int group;               // tokens whose angles a CTA holds (set by the launch)
 };
 
+// Most stretches an mx_attn_decode call splits a sequence into
+constexpr int kAttnMaxSplits = 512;
+
+// mx_attn_decode: one query token per sequence over a paged cache
+struct AttnParams {
+    const void *q;
+    int64_t ldq;
+    int q_fp32, q_vec;       // q_vec: every head starts on a 16-byte boundary
+    int64_t seqs;
+    int q_heads, kv_heads, head_dim;
+    const uint8_t *k_codes, *v_codes, *k_scales, *v_scales;
+    int64_t scale_bytes;     // of each of the two scale buffers
+    const float *k_ts, *v_ts;
+    int sfmt, log2B;
+    int pages, page_size, page_shift;   // page_shift: log2 page_size, or -1
+    const int32_t *table;
+    int64_t ld_table;
+    int max_pages;           // entries of a table row
+    const int32_t *lengths;
+    float scale;
+    int window, sinks;
+    void *out;
+    int64_t ldo;
+    int o_fp32;
+    float *lse;
+    int splits;
+    float2 *part_ml;         // [seqs][q_heads][splits]: reference, sum
+    float *part_o;           // [seqs][q_heads][splits][head_dim]
+    int group, head_groups;  // query heads per key head; warps per key head (set by the launch)
+    int64_t tasks;
+};
+
 // per-launch helpers implemented in the .cu files
 int launch_quantize(const QParams &p, int axis, int in_fp32, int fast, cudaStream_t st,
                     int *grid_out);
@@ -141,6 +173,8 @@ int cached_occupancy(const void *kernel, int threads, size_t smem);
 // per (kernel, device); 0 on success.
 int raise_smem_limit(const void *kernel, int bytes);
 int launch_gemv(GvParams p, cudaStream_t st);
+int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens);
+int launch_attn(AttnParams p, int el, int hp, cudaStream_t st);
 int launch_kv_append(KvAppendParams p, int head_dim, int in_fp32, cudaStream_t st);
 
 // Programmatic dependent launch: a CTA lets the next launch on the stream

@@ -129,3 +129,50 @@ def test_append_binding_refusals(mx):
     small.k.codes = small.k.codes[:8]
     with pytest.raises(ValueError):
         small.ref()
+
+
+def attn(mx, cfg, c, q=4096, qd=0, ldq=256, S=2, Hq=4, tab=4096, ldt=3, mp=3, ln=4096, scale=0.1, win=0, sinks=0, out=4096, od=0,
+         ldo=256, lse=None, ws=4096, wb=1 << 40):
+    p = lambda x: None if x is None else P(x)  # noqa: E731
+    return mx.mx_attn_decode(cfg, c, p(q), qd, ldq, S, Hq, p(tab), ldt, mp, p(ln), scale, win, sinks, p(out), od, ldo, p(lse),
+                             p(ws), wb, None)
+
+
+@pytest.mark.parametrize("cfg,rc", CACHE_CONFIGS)
+def test_attention_configurations(mx, cfg, rc):
+    assert attn(mx, mx.Config(**cfg), cache(mx)) == rc
+
+
+@pytest.mark.parametrize("args,rc", CACHES)
+def test_attention_caches(mx, args, rc):
+    assert attn(mx, mx.MXFP4, cache(mx, **args)) == rc
+
+
+@pytest.mark.parametrize("args,rc", [
+    (dict(qd=2), -1), (dict(od=3), -1), (dict(S=-1), -1), (dict(S=(1 << 20) + 1), -1), (dict(Hq=0), -1), (dict(Hq=3), -1),
+    (dict(mp=-1), -1), (dict(mp=1 << 28, ldt=1 << 28), -1), (dict(win=-1), -1), (dict(sinks=-2), -1),
+    (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),
+    (dict(q=None), -1), (dict(out=None), -1), (dict(ln=None), -1), (dict(tab=None), -1),
+    (dict(ldq=255), -1), (dict(ldo=255), -1), (dict(ldt=2), -1),
+    (dict(q=4097), -3), (dict(q=4098, qd=1), -3), (dict(out=4097), -3), (dict(tab=4098), -3), (dict(ln=4098), -3), (dict(lse=4098), -3),
+    (dict(mp=1000, ldt=1000, ws=None), -5), (dict(mp=1000, ldt=1000, wb=1000), -5), (dict(mp=1000, ldt=1000, ws=4104), -3),
+    (dict(S=0), 0),
+])
+def test_attention_arguments(mx, args, rc):
+    assert attn(mx, mx.MXFP4, cache(mx), **args) == rc
+
+
+def test_attention_workspace_size(mx):
+    L = mx.lib()
+    c = cache(mx, pages=1 << 12, page_size=64, dim=128)
+    assert L.mx_attn_workspace_bytes(c, 0, 4, 10, 0, 0) == 0 and L.mx_attn_workspace_bytes(None, 1, 4, 10, 0, 0) == 0
+    assert L.mx_attn_workspace_bytes(c, 1, 4, 1, 0, 0) == 0                       # one page: not split
+    long, short = L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 0, 0), L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 500, 4)
+    assert long > short > 0 and long % (4 * (8 + 512)) == 0
+
+
+def test_attention_binding_refusals(mx):
+    import torch
+    c = mx.kv_cache(2, 4, 1, 64, device="cpu")
+    with pytest.raises(ValueError):
+        mx.attn_decode(c, torch.zeros(1, 1, 64), torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
