@@ -10,17 +10,20 @@ namespace mxk {
 
 namespace {
 
-constexpr int kJoinThreads = 256;
+constexpr int kJoinCols = 64;   // elements of a head a join CTA takes
 
-// One CTA per (sequence, query head): the splits' sums brought to the common
-// maximum and added in order.  Each of the CTA's groups of D threads takes
-// every (256 / D)-th split; the groups' sums meet in shared memory.
-__global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constant__ AttnParams p)
+// One CTA per (sequence, query head, 64 elements of the head): the splits'
+// sums brought to the common maximum and added in a fixed order.  Groups of 16
+// threads hold the 64 elements and take every (threads / 16)-th split; the
+// groups' sums meet in shared memory.  Every warp finds the common maximum and
+// sum of weights by itself, so that one barrier is all.
+__global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnParams p)
 {
-    __shared__ float red[kJoinThreads];
-    __shared__ float wl[kJoinThreads / 32][2];
-    const int D = p.head_dim, groups = kJoinThreads / D, d = threadIdx.x % D, grp = threadIdx.x / D;
-    const int64_t out = blockIdx.x;                     // sequence * q_heads + head
+    __shared__ float4 red[512];
+    const int lane = threadIdx.x & 31, groups = blockDim.x / 16, d4 = threadIdx.x & 15, grp = threadIdx.x / 16;
+    const int D = p.head_dim, chunks = D / kJoinCols;
+    const int64_t out = blockIdx.x / chunks;            // sequence * q_heads + head
+    const int d = (blockIdx.x % chunks) * kJoinCols + 4 * d4;
     const int seq = (int)(out / p.q_heads), head = (int)(out % p.q_heads);
     pdl_trigger();
     pdl_wait();
@@ -30,36 +33,50 @@ __global__ void __launch_bounds__(kJoinThreads) k_attn_join(const __grid_constan
     const int used = per ? (tiles + per - 1) / per : 0;
     const float2 *ml = p.part_ml + out * p.splits;
     float m = -INFINITY;
-    for (int s = threadIdx.x; s < used; s += kJoinThreads) m = fmaxf(m, ml[s].x);
+    for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    if ((threadIdx.x & 31) == 0) wl[threadIdx.x >> 5][0] = m;
-    __syncthreads();
-    for (int i = 0; i < kJoinThreads / 32; ++i) m = fmaxf(m, wl[i][0]);
-    float l = 0.0f, o = 0.0f;
+    // a stretch without a visible token has m = -inf, l = 0; one whose scores
+    // are NaN makes the result NaN
+    const auto weight = [m](float2 x) { return x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : exp2f(x.x - m); };
+    float l = 0.0f;
+    for (int s = lane; s < used; s += 32) {
+        const float2 x = ml[s];
+        l = fmaf(weight(x), x.y, l);
+    }
+#pragma unroll
+    for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    const float *part = p.part_o + out * p.splits * D + d;
 #pragma unroll 4
     for (int s = grp; s < used; s += groups) {
-        const float2 x = ml[s];
-        // a stretch without a visible token has m = -inf, l = 0; one whose
-        // scores are NaN makes the result NaN
-        const float w = x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : exp2f(x.x - m);
-        l = fmaf(w, x.y, l);
-        o = fmaf(w, p.part_o[(out * p.splits + s) * D + d], o);
+        const float w = weight(ml[s]);
+        const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * D);
+        o.x = fmaf(w, v.x, o.x);
+        o.y = fmaf(w, v.y, o.y);
+        o.z = fmaf(w, v.z, o.z);
+        o.w = fmaf(w, v.w, o.w);
     }
     red[threadIdx.x] = o;
     __syncthreads();
-    if (grp == 0)
-        for (int i = 1; i < groups; ++i) o += red[i * D + d];
-    __syncthreads();
-    red[threadIdx.x] = l;
-    __syncthreads();
     if (grp) return;
-    for (int i = 1; i < groups; ++i) l += red[i * D + d];
+    for (int i = 1; i < groups; ++i) {
+        const float4 v = red[i * 16 + d4];
+        o.x += v.x;
+        o.y += v.y;
+        o.z += v.z;
+        o.w += v.w;
+    }
     const bool any = l > 0.0f || l != l;
-    const float v = any ? __fdiv_rn(o, l) : 0.0f;
+    const float inv = any ? __fdiv_rn(1.0f, l) : 0.0f;
+    const float v[4] = {o.x, o.y, o.z, o.w};
     const int64_t at = (int64_t)seq * p.ldo + (int64_t)head * D + d;
-    if (p.o_fp32) static_cast<float *>(p.out)[at] = v;
-    else static_cast<__nv_bfloat16 *>(p.out)[at] = __float2bfloat16_rn(v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = any ? __fmul_rn(v[i], inv) : 0.0f;
+        if (p.o_fp32) static_cast<float *>(p.out)[at + i] = y;
+        else static_cast<__nv_bfloat16 *>(p.out)[at + i] = __float2bfloat16_rn(y);
+    }
     if (d == 0 && p.lse) p.lse[out] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
 }
 
@@ -101,12 +118,14 @@ int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
     const int nth = p.group <= 4 ? 1 : 2;
     p.head_groups = (p.group + 4 * nth - 1) / (4 * nth);
     p.tasks = p.seqs * p.splits * p.head_groups * p.kv_heads;
-    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : 32, nth, hp);
+    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp);
     if (k.smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(k.k), k.smem)) return 1;
     const int64_t ctas = (p.tasks + kAtWarps - 1) / kAtWarps;
     if (launch_pdl(k.k, (unsigned)ctas, kAtThreads, k.smem, st, p) != cudaSuccess) return 1;
     if (p.splits == 1) return 0;
-    return launch_pdl(k_attn_join, (unsigned)(p.seqs * p.q_heads), kJoinThreads, 0, st, p) == cudaSuccess ? 0 : 1;
+    int groups = 4;
+    while (groups < 32 && groups < p.splits) groups *= 2;
+    return launch_pdl(k_attn_join, (unsigned)(p.seqs * p.q_heads * (p.head_dim / kJoinCols)), groups * 16, 0, st, p) == cudaSuccess ? 0 : 1;
 }
 
 }  // namespace mxk

@@ -57,16 +57,23 @@ template <int EL, int D, int BS> struct AtGeom {
     static constexpr int NPC = ROW / 16;               // 16-byte pieces
     // bytes kept of a token's scales: all of them (blocks of 16), a word at least
     static constexpr int SW = BS == 16 ? D / 16 : (D / 32 < 4 ? 4 : D / 32);
+    // scales that may be fewer bytes than a word: found in the aligned word
+    // around them (BS 64 stands for blocks of 64 and 128)
+    static constexpr bool NARROW = BS == 64 || (BS == 32 && D == 64);
     static constexpr int K_AT = 0, V_AT = 16 * ROW, KS_AT = 32 * ROW, VS_AT = KS_AT + 16 * SW, META_AT = VS_AT + 16 * SW;
-    static constexpr int STAGE = META_AT + 16;
+    // a stage is a multiple of a row, so that a row's pieces are reached by an
+    // exclusive or of its address
+    static constexpr int STAGE = (META_AT + 16 + ROW - 1) / ROW * ROW;
     static constexpr int STAGES = STAGE * 4 * kAtWarps <= 48 * 1024 ? 4 : 3;
     // piece swizzle by row: the eight rows a K read touches at once, and the
-    // four of a V read, fall on different banks
+    // four of a V read, fall on different banks.  Rows 8 apart have the same,
+    // and of row t + 4 i (t < 4) it is swz(t) ^ swz4(i).
     static __host__ __device__ constexpr int swz(int row)
     {
         return BITS == 8 && NPC == 4 ? (row & 2) | ((row >> 2) & 1) : BITS == 8 ? ((row & 3) << 1) | ((row >> 2) & 1)
                : NPC == 2 ? (row >> 2) & 1 : NPC == 4 ? (row >> 1) & 3 : row & 7;
     }
+    static __host__ __device__ constexpr int swz4(int i) { return swz(4 * (i & 1)); }
 };
 
 __device__ __forceinline__ void cp_async_n(uint32_t dst, const void *src, int n, int src_bytes)
@@ -75,84 +82,115 @@ __device__ __forceinline__ void cp_async_n(uint32_t dst, const void *src, int n,
     else if (n == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
-__device__ __forceinline__ uint2 lds64(uint32_t a)
+// shared loads at an immediate offset
+template <int OFF> __device__ __forceinline__ uint2 lds64(uint32_t a)
 {
     uint2 r;
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(r.x), "=r"(r.y) : "r"(a), "n"(OFF));
     return r;
 }
-// two codes (a byte of 4-bit codes, or 16 bits of FP6) -> f16x2
-template <int EL> __device__ __forceinline__ uint32_t pair_half2(uint32_t c)
+template <int OFF> __device__ __forceinline__ uint32_t lds32(uint32_t a)
 {
     uint32_t r;
-    if (EL == GE_E2M1) {
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(r) : "r"(c));
-    } else if (EL == AE_E2M3) {
-        asm("cvt.rn.f16x2.e2m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
-    } else if (EL == AE_E3M2) {
-        asm("cvt.rn.f16x2.e3m2x2 %0, %1;" : "=r"(r) : "h"((uint16_t)c));
-    } else {
-        uint32_t h[4];
-        codes8_halves<EL>(c & 0xffu, h);
-        r = h[0];
-    }
+    asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(r) : "r"(a), "n"(OFF));
+    return r;
+}
+template <int OFF> __device__ __forceinline__ uint32_t lds16(uint32_t a)
+{
+    uint16_t r;
+    asm volatile("ld.shared.b16 %0, [%1+%2];" : "=h"(r) : "r"(a), "n"(OFF));
     return r;
 }
 
-// Eight codes of lane t in 32-block b of a key row -> four f16x2.
-template <int EL, int D, int BS>
-__device__ __forceinline__ void at_key_codes(uint32_t kt, int row, int b, int t, uint32_t h[4])
+// 2^x, good to 2 ulp; results below 2^-126 are zero
+__device__ __forceinline__ float ex2(float x)
 {
-    using G = AtGeom<EL, D, BS>;
-    const int z = G::swz(row);
-    if constexpr (G::BITS == 4) {
-        const uint32_t p = kt + row * G::ROW + ((b ^ z) << 4);
-        uint32_t w;
-        if (BS == 16) w = __byte_perm(lds32(p + 4 * (t >> 1)), lds32(p + 8 + 4 * (t >> 1)), (t & 1) ? 0x7632u : 0x5410u);
-        else w = lds32(p + 4 * t);
-        codes8_halves<EL>(w, h);
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// x as f16 in both halves
+__device__ __forceinline__ uint32_t half2_of(float x)
+{
+    const __half2 h = __floats2half2_rn(x, x);
+    return *reinterpret_cast<const uint32_t *>(&h);
+}
+
+// two code pairs (16 bits of 4-bit codes, 32 of FP6) -> two f16x2
+template <int EL> __device__ __forceinline__ void pairs2(uint32_t c, uint32_t &lo, uint32_t &hi)
+{
+    if (EL == GE_E2M1) {
+        // (each from the low byte of a register: the conversion of another
+        // byte of a value loaded in 16 bits came out wrong with nvcc 12.9)
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(lo) : "r"(c));
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(hi) : "r"(c >> 8));
+    } else if (EL == AE_E2M3) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e2m3x2 %0, a;\n\tcvt.rn.f16x2.e2m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(c));
+    } else if (EL == AE_E3M2) {
+        asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e3m2x2 %0, a;\n\tcvt.rn.f16x2.e3m2x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(c));
     } else {
-        // blocks of 16: four codes of each half of the 32-block
-        uint2 w;
-        if (BS == 16) {
-            w.x = lds32(kt + row * G::ROW + (((2 * b) ^ z) << 4) + 4 * t);
-            w.y = lds32(kt + row * G::ROW + (((2 * b + 1) ^ z) << 4) + 4 * t);
-        } else {
-            w = lds64(kt + row * G::ROW + (((2 * b + (t >> 1)) ^ z) << 4) + 8 * (t & 1));
-        }
-        h[0] = pair_half2<EL>(w.x);
-        h[1] = pair_half2<EL>(w.x >> 16);
-        h[2] = pair_half2<EL>(w.y);
-        h[3] = pair_half2<EL>(w.y >> 16);
+        uint32_t h[4];
+        codes8_halves<EL>(c, h);
+        lo = h[0];
+        hi = h[1];
     }
 }
 
-// Code pairs 2g, 2g + 1 (blocks of 16: g and g + 8) of 32-block b of a value
-// row -> the operand's rows g and g + 8.
-template <int EL, int D, int BS>
-__device__ __forceinline__ void at_value_codes(uint32_t vt, int row, int b, int g, uint32_t &lo, uint32_t &hi)
+// Eight codes of lane t in 32-block b of a key row -> four f16x2.  at: the
+// lane's place in row g, swizzle and lane part of the piece included; OFF: to
+// the row.
+template <int EL, int D, int BS, int OFF>
+__device__ __forceinline__ void at_key_codes(uint32_t at, int b, int t, uint32_t h[4])
 {
     using G = AtGeom<EL, D, BS>;
-    const int z = G::swz(row);
-    const uint32_t r = vt + row * G::ROW;
     if constexpr (G::BITS == 4) {
-        const uint32_t p = r + ((b ^ z) << 4);
-        if (BS == 16) {
-            lo = pair_half2<EL>(lds16(p + (g & 6)) >> (8 * (g & 1)));
-            hi = pair_half2<EL>(lds16(p + 8 + (g & 6)) >> (8 * (g & 1)));
-        } else {
-            const uint32_t w = lds16(p + 2 * g);
-            lo = pair_half2<EL>(w);
-            hi = pair_half2<EL>(w >> 8);
-        }
-    } else if (BS == 16) {
-        lo = pair_half2<EL>(lds16(r + (((2 * b) ^ z) << 4) + 2 * g));
-        hi = pair_half2<EL>(lds16(r + (((2 * b + 1) ^ z) << 4) + 2 * g));
+        const uint32_t p = at ^ (b << 4);
+        uint32_t w;
+        if (BS == 16) w = __byte_perm(lds32<OFF>(p), lds32<OFF + 8>(p), (t & 1) ? 0x7632u : 0x5410u);
+        else w = lds32<OFF>(p);
+        codes8_halves<EL>(w, h);
     } else {
-        const uint32_t w = lds32(r + (((2 * b + (g >> 2)) ^ z) << 4) + 4 * (g & 3));
-        lo = pair_half2<EL>(w);
-        hi = pair_half2<EL>(w >> 16);
+        uint2 w;
+        if (BS == 16) w = make_uint2(lds32<OFF>(at ^ (b << 5)), lds32<OFF>(at ^ (b << 5) ^ 16));   // four codes of each half
+        else w = lds64<OFF>(at ^ (b << 5));
+        pairs2<EL>(w.x, h[0], h[1]);
+        pairs2<EL>(w.y, h[2], h[3]);
     }
+}
+template <int EL, int D, int BS> __device__ __forceinline__ uint32_t at_key_lane(int g, int t)
+{
+    using G = AtGeom<EL, D, BS>;
+    const uint32_t row = g * G::ROW + (G::swz(g) << 4);
+    if (G::BITS == 4) return row + (BS == 16 ? 4 * (t >> 1) : 4 * t);
+    return BS == 16 ? row + 4 * t : (row ^ ((t >> 1) << 4)) + 8 * (t & 1);
+}
+
+// Code pairs 2g, 2g + 1 (blocks of 16: g and g + 8) of 32-block b of value row
+// t + 4 I -> the operand's rows g and g + 8.  at: the lane's place in row t.
+template <int EL, int D, int BS, int I>
+__device__ __forceinline__ void at_value_codes(uint32_t at, int b, int g, uint32_t &lo, uint32_t &hi)
+{
+    using G = AtGeom<EL, D, BS>;
+    constexpr int OFF = 4 * I * G::ROW;
+    if constexpr (G::BITS == 4) {
+        const uint32_t p = at ^ ((b ^ G::swz4(I)) << 4);
+        // (blocks of 16: byte g of each half, read as the 16 bits around it)
+        const uint32_t w = BS == 16 ? __byte_perm(lds16<OFF>(p), lds16<OFF + 8>(p), (g & 1) ? 0x4451u : 0x4440u) : lds16<OFF>(p);
+        pairs2<EL>(w, lo, hi);
+    } else {
+        const uint32_t p = at ^ (((2 * b) ^ G::swz4(I)) << 4);
+        const uint32_t w = BS == 16 ? __byte_perm(lds16<OFF>(p), lds16<OFF>(p ^ 16), 0x5410u) : lds32<OFF>(p);
+        pairs2<EL>(w, lo, hi);
+    }
+}
+template <int EL, int D, int BS> __device__ __forceinline__ uint32_t at_value_lane(int g, int t)
+{
+    using G = AtGeom<EL, D, BS>;
+    const uint32_t row = G::V_AT + t * G::ROW + (G::swz(t) << 4);
+    if (G::BITS == 4) return row + (BS == 16 ? (g & 6) : 2 * g);
+    return BS == 16 ? row + 2 * g : (row ^ ((g >> 2) << 4)) + 4 * (g & 3);
 }
 
 // A token's scales -> binary32, one per 32-block (two with blocks of 16).
@@ -167,15 +205,16 @@ __device__ __forceinline__ void at_scales(const AttnParams &p, uint32_t area, in
         for (int i = 0; i < G::SW / 4; ++i) scales4(p.sfmt, lds32(a + 4 * i), s + 4 * i);
         return;
     }
-    uint32_t w0 = lds32(a) >> shifts, w1 = 0u;
+    uint32_t w0 = lds32(a), w1 = 0u;
     if (G::SW > 4) w1 = lds32(a + 4);
+    if (G::NARROW) w0 >>= shifts;
     float f[4];
-    scales4(p.sfmt, __byte_perm(w0, w1, sel[0]), f);
+    scales4(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[0]) : w0, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (i < G::NB) s[i] = f[i];
     if (G::NB > 4) {
-        scales4(p.sfmt, __byte_perm(w0, w1, sel[1]), f);
+        scales4(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[1]) : w1, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (4 + i < G::NB) s[4 + i] = f[i];
@@ -230,7 +269,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
 {
     using G = AtGeom<EL, D, BS>;
     constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(256) uint8_t smem_at[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     pdl_trigger();
@@ -252,14 +291,14 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
     const int tile0 = split * per, tile1 = min(tile0 + per, tiles);
     if (tile0 >= tile1 && p.splits > 1) return;   // (the join reads no more than the splits in use)
 
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem) + warp * G::STAGES * G::STAGE;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_at) + warp * G::STAGES * G::STAGE;
     const int skip = n - vis;                 // tokens between the sinks and the window
     const int32_t *table = p.table + (int64_t)seq * p.ld_table;
     const int nsc = D >> p.log2B;             // scales of a head
-    const int64_t code_row = (int64_t)p.kv_heads * G::ROW, sc_row = (int64_t)p.kv_heads * nsc;
+    const uint32_t code_row = (uint32_t)p.kv_heads * G::ROW, sc_row = (uint32_t)(p.kv_heads * nsc);   // (under 2^20)
     const uint8_t *kc = p.k_codes + kh * G::ROW, *vc = p.v_codes + kh * G::ROW;
     // lanes 0..15 copy key scales of their token, 16..31 value scales
-    const uint8_t *sc = lane < 16 ? p.k_scales : p.v_scales;
+    const uint8_t *sc = (lane < 16 ? p.k_scales : p.v_scales) + (G::NARROW ? 0 : kh * nsc);
 
     // page number of the lane's token (lane & 15) in a tile; -1 behind the end
     auto page_of = [&](int tile, int &off) {
@@ -274,37 +313,41 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
     uint32_t st_w = ring;
     auto issue = [&]() {
         if (it < tile1) {
-            const bool ok = next_page >= 0 && next_page < p.pages;
-            const int row = ok ? next_page * p.page_size + next_off : -1;
+            const bool ok = (uint32_t)next_page < (uint32_t)p.pages;
+            const uint32_t row = ok ? (uint32_t)(next_page * p.page_size + next_off) : 0u;
+            const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;   // the tokens that are there
             ++it;
             next_page = page_of(it, next_off);
 #pragma unroll
             for (int i = 0; i < G::NPC / 2; ++i) {
                 const int idx = i * 32 + lane, r = idx / G::NPC, pc = idx % G::NPC;
-                const int src = __shfl_sync(0xffffffffu, row, r);
-                const int64_t at = src < 0 ? 0 : (int64_t)src * code_row + pc * 16;
+                const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, row, r) * code_row + pc * 16;
+                const int nb = (mask >> r) & 1 ? 16 : 0;
                 const uint32_t dst = st_w + r * G::ROW + ((pc ^ G::swz(r)) << 4);
-                cp_async16(dst + G::K_AT, kc + at, src < 0 ? 0 : 16);
-                cp_async16(dst + G::V_AT, vc + at, src < 0 ? 0 : 16);
+                cp_async16(dst + G::K_AT, kc + at, nb);
+                cp_async16(dst + G::V_AT, vc + at, nb);
             }
-            int shift = 0;
-            {
-                const int64_t at = row < 0 ? 0 : (int64_t)row * sc_row + kh * nsc;
-                const uint32_t dst = st_w + (lane < 16 ? G::KS_AT : G::VS_AT) + (lane & 15) * G::SW;
+            const uint32_t dst = st_w + (lane < 16 ? G::KS_AT : G::VS_AT) + (lane & 15) * G::SW;
+            if (!G::NARROW) {
+                // (BS 32: a byte per 32-block, BS 16: two)
+                cp_async_n(dst, sc + (uint64_t)row * sc_row, G::SW, ok ? G::SW : 0);
+                if (lane == 0) asm volatile("st.shared.b32 [%0], %1;" ::"r"(st_w + G::META_AT), "r"(mask) : "memory");
+            } else {
+                const uint64_t at = (uint64_t)row * sc_row + kh * nsc;
+                int shift = 0;
                 if (nsc >= 4) {
-                    cp_async_n(dst, sc + at, nsc, row < 0 ? 0 : nsc);
+                    cp_async_n(dst, sc + at, nsc, ok ? nsc : 0);
                 } else {
                     // one or two bytes: the aligned word around them
                     shift = (int)(at & 3);
-                    const int64_t w = at & ~(int64_t)3;
-                    cp_async_n(dst, sc + w, 4, row < 0 ? 0 : (int)min((int64_t)4, p.scale_bytes - w));
+                    const uint64_t w = at & ~(uint64_t)3;
+                    cp_async_n(dst, sc + w, 4, ok ? (int)min((int64_t)4, p.scale_bytes - (int64_t)w) : 0);
                 }
+                const uint32_t b0 = __ballot_sync(0xffffffffu, shift & 1), b1 = __ballot_sync(0xffffffffu, shift & 2);
+                if (lane == 0)
+                    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(st_w + G::META_AT), "r"(mask), "r"(b0 & 0xffffu),
+                                 "r"(b1 & 0xffffu), "r"(0u) : "memory");
             }
-            const uint32_t mask = __ballot_sync(0xffffffffu, ok);
-            const uint32_t b0 = __ballot_sync(0xffffffffu, shift & 1), b1 = __ballot_sync(0xffffffffu, shift & 2);
-            if (lane == 0)
-                asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(st_w + G::META_AT), "r"(mask & 0xffffu), "r"(b0 & 0xffffu),
-                             "r"(b1 & 0xffffu), "r"(0u) : "memory");
         }
         st_w = st_w + G::STAGE == ring + G::STAGES * G::STAGE ? ring : st_w + G::STAGE;
         cp_async_commit();
@@ -379,26 +422,30 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
             for (int i = 0; i < 4; ++i) acc[q][j][i] = 0.0f;
     }
 
+    const uint32_t k_lane = at_key_lane<EL, D, BS>(g, t), v_lane = at_value_lane<EL, D, BS>(g, t);
+    uint32_t lim[(G::SW + 7) / 8] = {};       // limits of the lane's share of value scale bytes
     uint32_t st = ring;
     for (int tile = tile0; tile < tile1; ++tile) {
         cp_async_wait<G::STAGES - 2>();
         __syncwarp();                         // the tile is in, and the last one is read
         issue();
-        const uint4 meta = lds128(st + G::META_AT);
+        uint4 meta;
+        if (G::NARROW) meta = lds128(st + G::META_AT);
+        else meta = make_uint4(lds32(st + G::META_AT), 0u, 0u, 0u);
+        // where a token's scales begin in their word
+        const auto shift_of = [&](int tk) { return G::NARROW ? (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8 : 0u; };
 
         // scores of tokens g, g + 8 (heads 2t, 2t + 1)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         {
             float kl[NB * SUB], kg[NB * SUB];
-            const int sl = (((meta.y >> g) & 1) | (((meta.z >> g) & 1) << 1)) * 8;
-            const int sh = (((meta.y >> (g + 8)) & 1) | (((meta.z >> (g + 8)) & 1) << 1)) * 8;
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g, sl, sel, kl);
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, sh, sel, kg);
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g, shift_of(g), sel, kl);
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, shift_of(g + 8), sel, kg);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint32_t lo[4], hi[4];
-                at_key_codes<EL, D, BS>(st + G::K_AT, g, b, t, lo);
-                at_key_codes<EL, D, BS>(st + G::K_AT, g + 8, b, t, hi);
+                at_key_codes<EL, D, BS, 0>(st + k_lane, b, t, lo);
+                at_key_codes<EL, D, BS, 8 * G::ROW>(st + k_lane, b, t, hi);
 #pragma unroll
                 for (int u = 0; u < SUB; ++u) {
                     float d[4], e[4];
@@ -424,11 +471,14 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
                 }
             }
         }
-        const bool on_l = (meta.x >> g) & 1, on_h = (meta.x >> (g + 8)) & 1;
-        s[0] = on_l ? __fmul_rn(s[0], fac0) : -INFINITY;
-        s[1] = on_l ? __fmul_rn(s[1], fac1) : -INFINITY;
-        s[2] = on_h ? __fmul_rn(s[2], fac0) : -INFINITY;
-        s[3] = on_h ? __fmul_rn(s[3], fac1) : -INFINITY;
+        s[0] = __fmul_rn(s[0], fac0);
+        s[1] = __fmul_rn(s[1], fac1);
+        s[2] = __fmul_rn(s[2], fac0);
+        s[3] = __fmul_rn(s[3], fac1);
+        if (meta.x != 0xffffu) {
+            if (!((meta.x >> g) & 1)) s[0] = s[1] = -INFINITY;
+            if (!((meta.x >> (g + 8)) & 1)) s[2] = s[3] = -INFINITY;
+        }
 
         // move the reference when a score passes it by 2^4
         if (__any_sync(0xffffffffu, fmaxf(s[0], s[2]) > m0 + 4.0f || fmaxf(s[1], s[3]) > m1 + 4.0f)) {
@@ -438,7 +488,7 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
                 a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, d));
                 c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, d));
             }
-            const float r0 = m0 == a ? 1.0f : exp2f(m0 - a), r1 = m1 == c ? 1.0f : exp2f(m1 - c);
+            const float r0 = m0 == a ? 1.0f : ex2(m0 - a), r1 = m1 == c ? 1.0f : ex2(m1 - c);
             m0 = a;
             m1 = c;
             l0 *= r0;
@@ -455,25 +505,38 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
             }
         }
         const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
-        s[0] = exp2f(s[0] - b0);
-        s[1] = exp2f(s[1] - b1);
-        s[2] = exp2f(s[2] - b0);
-        s[3] = exp2f(s[3] - b1);
+        s[0] = ex2(s[0] - b0);
+        s[1] = ex2(s[1] - b1);
+        s[2] = ex2(s[2] - b0);
+        s[3] = ex2(s[3] - b1);
         l0 += s[0] + s[2];
         l1 += s[1] + s[3];
 
         // value scales of tokens t, t + 4, t + 8, t + 12
         float vs[4][NB * SUB];
-        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int tk = t + 4 * i;
-            at_scales<EL, D, BS>(p, st + G::VS_AT, tk, (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8, sel, vs[i]);
+        for (int i = 0; i < 4; ++i) at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, vs[i]);
+        // a scale past 2^3 times its block's reference, or none yet: the codes
+        // of scales order like their values, so each lane compares its share of
+        // the tile's scale bytes
+        bool past = false;
+        if (G::NARROW) {
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NB * SUB; ++j) top = fmaxf(top, __fmul_rn(vs[i][j], cb[j / SUB]));
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < NB * SUB; ++j) top = fmaxf(top, __fmul_rn(vs[i][j], cb[j / SUB]));
+            past = top > 8.0f || cb[0] == 0.0f;
+        } else {
+            const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
+#pragma unroll
+            for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                const uint32_t w = G::SW == 4 ? lds16(a) : lds32(a + 4 * i);
+#pragma unroll
+                for (int k = 0; k < (G::SW == 4 ? 2 : 4); ++k) past |= ((w >> (8 * k)) & 0xffu) > ((lim[i] >> (8 * k)) & 0xffu);
+            }
         }
-        // new reference exponents when a scale passes its own by 2^3, or at first
-        if (__any_sync(0xffffffffu, top > 8.0f || cb[0] == 0.0f)) {
+        if (__any_sync(0xffffffffu, past)) {
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
                 float x = 0.0f;
@@ -495,6 +558,23 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
                     cb[j] = c;
                 }
             }
+            if (!G::NARROW) {
+                // the limits of the lane's bytes: the code of 2^(E + 3)
+#pragma unroll
+                for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                    lim[i] = 0u;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int at = (lane * (G::SW / 2) + 4 * i + k) & (G::SW - 1);   // the byte's scale
+                        int e = 0;
+#pragma unroll
+                        for (int j = 0; j < NB; ++j)
+                            if (at / SUB == j) e = 127 - (int)(__float_as_uint(cb[j]) >> 23);
+                        const int code = p.sfmt == S_E8M0 ? e + 130 : (e + 3 + (p.sfmt == S_UE4M3 ? 7 : 15)) * 8;
+                        lim[i] |= (uint32_t)min(max(code, 0), 255) << (8 * k);
+                    }
+                }
+            }
         }
         // weights p of the lane's tokens and column head, times 2^7
         float pw[NTH][4];
@@ -510,12 +590,14 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
                 pw[q][2 + i] = __fmul_rn(odd ? y1 : y0, 128.0f);
             }
         }
-        const int par = (g & 1) * 16;               // the column's parity
+        const uint32_t par = (g & 1) ? 0xffff0000u : 0x0000ffffu;   // the column's parity
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t lo[4], hi[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) at_value_codes<EL, D, BS>(st + G::V_AT, t + 4 * i, j, g, lo[i], hi[i]);
+            at_value_codes<EL, D, BS, 0>(st + v_lane, j, g, lo[0], hi[0]);
+            at_value_codes<EL, D, BS, 1>(st + v_lane, j, g, lo[1], hi[1]);
+            at_value_codes<EL, D, BS, 2>(st + v_lane, j, g, lo[2], hi[2]);
+            at_value_codes<EL, D, BS, 3>(st + v_lane, j, g, lo[3], hi[3]);
 #pragma unroll
             for (int q = 0; q < NTH; ++q)
 #pragma unroll
@@ -524,9 +606,12 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const float x = __fmul_rn(__fmul_rn(pw[q][i], cb[j]), vs[i][j * SUB + u]);
-                        const __half h = __float2half_rn(x);
-                        w[0][i] = (uint32_t)__half_as_ushort(h) << par;
-                        if (HP) w[PC - 1][i] = (uint32_t)__half_as_ushort(__float2half_rn(__fmul_rn(__fsub_rn(x, __half2float(h)), 2048.0f))) << par;
+                        const uint32_t h = half2_of(x);
+                        w[0][i] = h & par;
+                        if (HP) {
+                            const float back = __low2float(*reinterpret_cast<const __half2 *>(&h));
+                            w[PC - 1][i] = half2_of(__fmul_rn(__fsub_rn(x, back), 2048.0f)) & par;
+                        }
                     }
                     // blocks of 16: rows below 8 are the first half's pairs,
                     // the others the second's, each against its own weights
@@ -616,7 +701,7 @@ template <int EL, int D, int BS> AtPick at_pick_nth(int nth, int hp)
 }
 template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp)
 {
-    return bs == 16 ? at_pick_nth<EL, D, 16>(nth, hp) : at_pick_nth<EL, D, 32>(nth, hp);
+    return bs == 16 ? at_pick_nth<EL, D, 16>(nth, hp) : bs == 32 ? at_pick_nth<EL, D, 32>(nth, hp) : at_pick_nth<EL, D, 64>(nth, hp);
 }
 
 // the kernels of one element kind and head length, in translation units of their own
