@@ -168,13 +168,14 @@ def mx_version() -> str:
 
 # ---- marshalling helpers --------------------------------------------------
 def _p(t: torch.Tensor | None):
-    return None if t is None else C.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> C.c_void_p:
-    if stream is None:
-        stream = torch.cuda.current_stream()
-    return C.c_void_p(stream.cuda_stream)
+def _stream(stream) -> int:
+    """The handle of the stream, or of the current one."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _dtype_code(t: torch.Tensor) -> int:
@@ -199,28 +200,24 @@ def _cuda2d(x: torch.Tensor, name: str) -> None:
 
 def query_sizes(cfg: Config, rows: int, cols: int) -> mx_sizes:
     s = mx_sizes()
-    c = cfg.c()
-    _check("mx_query_sizes", lib().mx_query_sizes(C.byref(c), rows, cols, C.byref(s)))
+    _check("mx_query_sizes", lib().mx_query_sizes(cfg.ref(), rows, cols, C.byref(s)))
     return s
 
 
 # ---- low-level calls (C names) -------------------------------------------
 def mx_quantize(cfg: Config, x, x_dtype, rows, cols, codes, scales, tensor_scale, macro, offsets,
                 stats, workspace, workspace_bytes, stream) -> int:
-    c = cfg.c()
-    return lib().mx_quantize(C.byref(c), x, x_dtype, rows, cols, codes, scales, tensor_scale,
+    return lib().mx_quantize(cfg.ref(), x, x_dtype, rows, cols, codes, scales, tensor_scale,
                              macro, offsets, stats, workspace, workspace_bytes, stream)
 
 
 def mx_quantize_group(cfg: Config, x_dtype, items, n, stream) -> int:
     """``items``: a ctypes array of ``mx_quantize_item``."""
-    c = cfg.c()
-    return lib().mx_quantize_group(C.byref(c), x_dtype, items, n, stream)
+    return lib().mx_quantize_group(cfg.ref(), x_dtype, items, n, stream)
 
 
 def mx_tensor_amax(cfg: Config, x, x_dtype, rows, cols, workspace, workspace_bytes, stream) -> int:
-    c = cfg.c()
-    return lib().mx_tensor_amax(C.byref(c), x, x_dtype, rows, cols, workspace, workspace_bytes, stream)
+    return lib().mx_tensor_amax(cfg.ref(), x, x_dtype, rows, cols, workspace, workspace_bytes, stream)
 
 
 def mx_stats_finalize(stats, stream) -> int:
@@ -236,23 +233,20 @@ def mx_quantize_noalloc(cfg: Config, x, x_dtype, rows, cols, codes, scales, tens
     """mx_quantize without a workspace argument, for callers that cannot
     allocate device memory; its scratch is a fixed array inside the library
     shared by all calls (order the calls on one stream)."""
-    c = cfg.c()
-    return lib().mx_quantize_noalloc(C.byref(c), x, x_dtype, rows, cols, codes, scales,
+    return lib().mx_quantize_noalloc(cfg.ref(), x, x_dtype, rows, cols, codes, scales,
                                      tensor_scale, macro, offsets, stats, stream)
 
 
 def mx_hadamard_quantize(cfg: Config, x, x_dtype, rows, cols, codes, scales, tensor_scale, macro,
                          offsets, stats, rotated, workspace, workspace_bytes, stream) -> int:
-    c = cfg.c()
-    return lib().mx_hadamard_quantize(C.byref(c), x, x_dtype, rows, cols, codes, scales,
+    return lib().mx_hadamard_quantize(cfg.ref(), x, x_dtype, rows, cols, codes, scales,
                                       tensor_scale, macro, offsets, stats, rotated, workspace,
                                       workspace_bytes, stream)
 
 
 def mx_dequantize(cfg: Config, codes, scales, tensor_scale, macro, offsets, rows, cols, out,
                   out_dtype, stream) -> int:
-    c = cfg.c()
-    return lib().mx_dequantize(C.byref(c), codes, scales, tensor_scale, macro, offsets, rows, cols,
+    return lib().mx_dequantize(cfg.ref(), codes, scales, tensor_scale, macro, offsets, rows, cols,
                                out, out_dtype, stream)
 
 
@@ -264,8 +258,7 @@ def mx_qsnr(x, x_dtype, xh, xh_dtype, rows, cols, block, axis, stats, per_block_
 
 def mx_gemm(ca: Config, cb: Config, Aq, Asf, Bq, Bsf, tsA, tsB, M, N, K, C_out, c_dtype,
             stream) -> int:
-    a, b = ca.c(), cb.c()
-    return lib().mx_gemm(C.byref(a), C.byref(b), Aq, Asf, Bq, Bsf, tsA, tsB, M, N, K, C_out,
+    return lib().mx_gemm(ca.ref(), cb.ref(), Aq, Asf, Bq, Bsf, tsA, tsB, M, N, K, C_out,
                          c_dtype, stream)
 
 
@@ -291,15 +284,13 @@ def mx_attn_decode(cfg: Config, cache, q, q_dtype, ldq, seqs, q_heads, page_tabl
 
 def mx_gemm_qsnr(ca: Config, cb: Config, A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB, stats,
                  workspace, workspace_bytes, stream) -> int:
-    a, b = ca.c(), cb.c()
-    return lib().mx_gemm_qsnr(C.byref(a), C.byref(b), A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB,
+    return lib().mx_gemm_qsnr(ca.ref(), cb.ref(), A, B, M, N, K, Aq, Asf, Bq, Bsf, tsA, tsB,
                               stats, workspace, workspace_bytes, stream)
 
 
 def mx_mbs_gemm_scales(cfg: Config, scales, macro, rows, cols, sf16, tensor_scale, workspace,
                        workspace_bytes, stream) -> int:
-    c = cfg.c()
-    return lib().mx_mbs_gemm_scales(C.byref(c), scales, macro, rows, cols, sf16, tensor_scale, workspace,
+    return lib().mx_mbs_gemm_scales(cfg.ref(), scales, macro, rows, cols, sf16, tensor_scale, workspace,
                                     workspace_bytes, stream)
 
 
@@ -527,33 +518,40 @@ _DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
 
 
 class _Launch:
-    """Device and stream of a call: the operands' device made current, and its
-    current stream (or the caller's ``stream``) both for the launch and for
-    what the call allocates."""
+    """Device and stream of a call that is not simply on the current ones: the
+    operands' device made current, and the caller's ``stream`` both for the
+    launch and for what the call allocates."""
 
     __slots__ = ("ctx",)
 
     def __init__(self, device, stream):
-        self.ctx = []
-        if device.index != torch.cuda.current_device():
-            self.ctx.append(torch.cuda.device(device))
+        self.ctx = [torch.cuda.device(device)]
         if stream is not None:
             self.ctx.append(torch.cuda.stream(stream))
 
     def __enter__(self):
         for c in self.ctx:
             c.__enter__()
-        return torch.cuda.current_stream().cuda_stream
 
     def __exit__(self, *e):
         for c in reversed(self.ctx):
             c.__exit__(*e)
 
 
-def _same_device(device, **tensors) -> None:
-    for name, t in tensors.items():
+def _elsewhere(device, stream) -> bool:
+    return stream is not None or device.index != torch.cuda.current_device()
+
+
+def _raw_stream(device) -> int:
+    return torch._C._cuda_getCurrentRawStream(device.index)
+
+
+def _same_device(device, *named) -> None:
+    """``named``: name, tensor or None, name, ..."""
+    for i in range(1, len(named), 2):
+        t = named[i]
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+            raise ValueError(f"{named[i - 1]} is on {t.device}, expected {device}")
 
 
 def _rows_of(t: torch.Tensor, name: str) -> int:
@@ -579,27 +577,34 @@ def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *
     be ready on it."""
     if not x.is_cuda:
         raise ValueError("x must be a CUDA tensor")
-    if x.dim() not in (1, 2) or x.shape[-1] != qw.cols:
-        raise ValueError(f"x must be [M, {qw.cols}] or [{qw.cols}], got {list(x.shape)}")
-    x2 = x if x.dim() == 2 else x[None]
-    M, N, K = x2.shape[0], qw.rows, qw.cols
-    ldx = _rows_of(x2, "x")
     dev = x.device
-    _same_device(dev, codes=qw.codes, scales=qw.scales, macro=qw.macro, offsets=qw.offsets, out=out,
-                 tensor_scale=qw.tensor_scale if qw.cfg.tensor_scale else None)
-    with _Launch(dev, stream) as st:
-        if out is None:
-            y = torch.empty((M, N), dtype=out_dtype or x.dtype, device=dev)
-        else:
-            if out.shape != x.shape[:-1] + (N,) or out.dtype != (out_dtype or out.dtype):
-                raise ValueError(f"out must be {list(x.shape[:-1]) + [N]} of {out_dtype or out.dtype}")
-            y = out if out.dim() == 2 else out[None]
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return gemv(x, qw, out_dtype, out=out)
+    N, K, shape = qw.rows, qw.cols, x.shape
+    if len(shape) not in (1, 2) or shape[-1] != K:
+        raise ValueError(f"x must be [M, {K}] or [{K}], got {list(shape)}")
+    x2 = x if len(shape) == 2 else x[None]
+    M = x2.shape[0]
+    ldx = _rows_of(x2, "x")
+    ts = qw.tensor_scale
+    _same_device(dev, "codes", qw.codes, "scales", qw.scales, "macro", qw.macro, "offsets", qw.offsets, "out", out,
+                 "tensor_scale", ts if qw.cfg.tensor_scale else None)
+    if out is None:
+        y = x.new_empty((M, N), dtype=out_dtype)
+        if y.dtype not in _DT:
+            raise TypeError(f"unsupported dtype {y.dtype} (bf16 or fp32)")
+        ldy = N
+    else:
+        if out.shape != shape[:-1] + (N,) or out.dtype != (out_dtype or out.dtype):
+            raise ValueError(f"out must be {list(shape[:-1]) + [N]} of {out_dtype or out.dtype}")
+        y = out if out.dim() == 2 else out[None]
         ldy = _rows_of(y, "out")
-        rc = mx_gemv(qw.cfg, x2.data_ptr(), _DT[x.dtype], ldx, M, qw.codes.data_ptr(), qw.scales.data_ptr(),
-                     _ptr_or_none(qw.tensor_scale), _ptr_or_none(qw.macro), _ptr_or_none(qw.offsets), N, K,
-                     y.data_ptr(), _DT[y.dtype], ldy, st)
-    _check("mx_gemv", rc)
-    return out if out is not None else y if x.dim() == 2 else y[0]
+    rc = lib().mx_gemv(qw.cfg.ref(), x2.data_ptr(), _DT[x.dtype], ldx, M, qw.codes.data_ptr(), qw.scales.data_ptr(),
+                       _p(ts), _p(qw.macro), _p(qw.offsets), N, K, y.data_ptr(), _DT[y.dtype], ldy, _raw_stream(dev))
+    if rc:
+        _check("mx_gemv", rc)
+    return out if out is not None else y if len(shape) == 2 else y[0]
 
 
 @dataclasses.dataclass
@@ -622,8 +627,8 @@ class KVCache:
         if r is None:
             rows, cols, bits = self.pages * self.page_size, self.kv_heads * self.head_dim, 8 if self.cfg.elem in FP6 else 4
             for name, t in (("k", self.k), ("v", self.v)):
-                _same_device(self.device, **{name + ".scales": t.scales, name + ".codes": t.codes,
-                                             name + ".tensor_scale": t.tensor_scale if self.cfg.tensor_scale else None})
+                _same_device(self.device, name + ".scales", t.scales, name + ".codes", t.codes,
+                             name + ".tensor_scale", t.tensor_scale if self.cfg.tensor_scale else None)
                 if (t.codes.numel() * t.codes.element_size() < rows * cols * bits // 8 or not t.codes.is_contiguous() or
                         t.scales.numel() < rows * (cols // self.cfg.block) or not t.scales.is_contiguous()):
                     raise ValueError(f"{name}: buffers too small for {rows} rows of {cols}, or not contiguous")
@@ -662,15 +667,18 @@ def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, cfg: Conf
 
 def _heads(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
     """Token stride of ``[T, heads * dim]`` or ``[T, heads, dim]`` with contiguous heads."""
-    if t.dim() == 3 and tuple(t.shape[1:]) == (heads, dim):
-        if (dim > 1 and t.stride(2) != 1) or (heads > 1 and t.stride(1) != dim):
+    shape, stride = t.shape, t.stride()
+    if len(shape) == 3 and shape[1] == heads and shape[2] == dim:
+        if stride[2] != 1 or (heads > 1 and stride[1] != dim):
             raise ValueError(f"the heads of {name} must be contiguous")
-    elif not (t.dim() == 2 and t.shape[1] == heads * dim and t.stride(1) == 1):
+    elif not (len(shape) == 2 and shape[1] == heads * dim and (stride[1] == 1 or heads * dim == 0)):
         raise ValueError(f"{name} must be [T, {heads * dim}] or [T, {heads}, {dim}] with contiguous heads, got "
-                         f"{list(t.shape)} with strides {t.stride()}")
-    if t.shape[0] > 1 and t.stride(0) < heads * dim:
+                         f"{list(shape)} with strides {stride}")
+    if shape[0] <= 1:
+        return heads * dim
+    if stride[0] < heads * dim:
         raise ValueError(f"the tokens of {name} overlap")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return stride[0]
 
 
 def _vector(t, n, dtype, device, name):
@@ -696,16 +704,22 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
     True or a tensor, the rotated keys, else None."""
     if not k.is_cuda:
         raise ValueError("k must be a CUDA tensor")
-    D, H, T, dev = cache.head_dim, cache.kv_heads, k.shape[0], cache.device
-    if k.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {k.dtype} (bf16 or fp32)")
-    _same_device(dev, k=k, v=v, q=q, q_out=q_out, k_out=k_out if isinstance(k_out, torch.Tensor) else None)
+    dev, dt = k.device, k.dtype
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return kv_append(cache, q, k, v, slots, positions, q_gain=q_gain, k_gain=k_gain, eps=eps, inv_freq=inv_freq,
+                             interleaved=interleaved, q_out=q_out, k_out=k_out)
+    D, H, T = cache.head_dim, cache.kv_heads, k.shape[0]
+    if dt not in _DT:
+        raise TypeError(f"unsupported dtype {dt} (bf16 or fp32)")
+    into = k_out if isinstance(k_out, torch.Tensor) else None
+    _same_device(dev, "the cache", cache.k.codes, "v", v, "q", q, "q_out", q_out, "k_out", into)
     ldk, ldv = _heads(k, H, D, "k"), _heads(v, H, D, "v")
     Hq = 0 if q is None else q.shape[1] if q.dim() == 3 else q.shape[1] // D
     ldq = 0 if q is None else _heads(q, Hq, D, "q")
-    for name, t in (("v", v), ("q", q), ("q_out", q_out), ("k_out", k_out if isinstance(k_out, torch.Tensor) else None)):
-        if t is not None and (t.dtype != k.dtype or t.shape[0] != T):
-            raise ValueError(f"{name} must have {T} tokens of {k.dtype}")
+    for name, t in (("v", v), ("q", q), ("q_out", q_out), ("k_out", into)):
+        if t is not None and (t.dtype != dt or t.shape[0] != T):
+            raise ValueError(f"{name} must have {T} tokens of {dt}")
     rot = 0 if inv_freq is None else 2 * inv_freq.numel()
     if rot and positions is None:
         raise ValueError("a rotation needs positions")
@@ -713,20 +727,22 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
     pf = _vector(inv_freq, rot // 2, torch.float32, dev, "inv_freq")
     pq, pk = _vector(q_gain, D, torch.float32, dev, "q_gain"), _vector(k_gain, D, torch.float32, dev, "k_gain")
     pl = _vector(slots, T, torch.int64, dev, "slots")
-    with _Launch(dev, stream) as st:
-        if q is not None and q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=k.dtype, device=dev)
-        if k_out is True:
-            k_out = torch.empty((T, H, D), dtype=k.dtype, device=dev)
-        elif k_out is False:
-            k_out = None
-        ldqo = 0 if q_out is None else _heads(q_out, Hq, D, "q_out")
-        ldko = 0 if k_out is None else _heads(k_out, H, D, "k_out")
-        rc = mx_kv_append(cache.cfg, cache.ref(), _ptr_or_none(q), k.data_ptr(), v.data_ptr(), _DT[k.dtype], ldq, ldk, ldv,
-                          T, Hq, pq, pk, eps, pf, rot, int(interleaved), ps, pl, _ptr_or_none(q_out), ldqo,
-                          _ptr_or_none(k_out), ldko, st)
-    _check("mx_kv_append", rc)
-    return q_out, k_out
+    ldqo, ldko = Hq * D, H * D
+    if q is None:
+        q_out = None
+    elif q_out is None:
+        q_out = k.new_empty((T, Hq, D))
+    else:
+        ldqo = _heads(q_out, Hq, D, "q_out")
+    if into is not None:
+        ldko = _heads(into, H, D, "k_out")
+    elif k_out is True:
+        into = k.new_empty((T, H, D))
+    rc = lib().mx_kv_append(cache.cfg.ref(), cache.ref(), _p(q), k.data_ptr(), v.data_ptr(), _DT[dt], ldq, ldk, ldv, T, Hq, pq, pk,
+                            eps, pf, rot, int(interleaved), ps, pl, _p(q_out), ldqo, _p(into), ldko, _raw_stream(dev))
+    if rc:
+        _check("mx_kv_append", rc)
+    return q_out, into
 
 
 def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, *,
@@ -742,36 +758,46 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengt
     ``[S, q_heads]``.  Scratch is allocated per call unless ``workspace`` (uint8) is given."""
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
-    D, dev, S = cache.head_dim, cache.device, q.shape[0]
+    dev = q.device
+    if _elsewhere(dev, stream):
+        with _Launch(dev, stream):
+            return attn_decode(cache, q, page_table, lengths, scale=scale, window=window, sinks=sinks, lse=lse,
+                               out_dtype=out_dtype, out=out, workspace=workspace)
+    D, S = cache.head_dim, q.shape[0]
     if q.dtype not in _DT:
         raise TypeError(f"unsupported dtype {q.dtype} (bf16 or fp32)")
-    _same_device(dev, q=q, page_table=page_table, out=out, workspace=workspace)
+    _same_device(dev, "the cache", cache.k.codes, "page_table", page_table, "out", out, "workspace", workspace)
     Hq = q.shape[1] if q.dim() == 3 else q.shape[1] // D
     ldq = _heads(q, Hq, D, "q")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != S:
         raise ValueError(f"page_table must be int32 [{S}, max_pages]")
-    pages = page_table.shape[1]
-    if (pages > 1 and page_table.stride(1) != 1) or (S > 1 and page_table.stride(0) < pages):
+    pages, (ldt, one) = page_table.shape[1], page_table.stride()
+    if (pages > 1 and one != 1) or (S > 1 and ldt < pages):
         raise ValueError("page_table must have contiguous rows")
-    ldt = page_table.stride(0) if S > 1 else pages
+    if S <= 1:
+        ldt = pages
     pl = _vector(lengths, S, torch.int32, dev, "lengths")
     if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
         raise ValueError("workspace must be contiguous uint8")
-    with _Launch(dev, stream) as st:
-        if out is None:
-            out = torch.empty((S, Hq, D), dtype=out_dtype or q.dtype, device=dev)
-        elif out.dtype not in _DT or out.shape[0] != S or out.dtype != (out_dtype or out.dtype):
-            raise ValueError(f"out must have {S} rows of {out_dtype or 'bf16 or fp32'}")
+    if out is None:
+        out = q.new_empty((S, Hq, D), dtype=out_dtype)
+        if out.dtype not in _DT:
+            raise TypeError(f"unsupported dtype {out.dtype} (bf16 or fp32)")
+        ldo = Hq * D
+    elif out.dtype not in _DT or out.shape[0] != S or out.dtype != (out_dtype or out.dtype):
+        raise ValueError(f"out must have {S} rows of {out_dtype or 'bf16 or fp32'}")
+    else:
         ldo = _heads(out, Hq, D, "out")
-        ref = cache.ref()
-        ls = torch.empty((S, Hq), dtype=torch.float32, device=dev) if lse else None
-        nbytes = lib().mx_attn_workspace_bytes(ref, S, Hq, pages, window, sinks)
-        if workspace is None and nbytes:
-            workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        rc = mx_attn_decode(cache.cfg, ref, q.data_ptr(), _DT[q.dtype], ldq, S, Hq, page_table.data_ptr(), ldt, pages, pl,
-                            D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _DT[out.dtype], ldo,
-                            _ptr_or_none(ls), _ptr_or_none(workspace), workspace.numel() if workspace is not None else 0, st)
-    _check("mx_attn_decode", rc)
+    L, ref = lib(), cache.ref()
+    ls = q.new_empty((S, Hq), dtype=torch.float32) if lse else None
+    nbytes = L.mx_attn_workspace_bytes(ref, S, Hq, pages, window, sinks)
+    if workspace is None and nbytes:
+        workspace = q.new_empty(nbytes, dtype=torch.uint8)
+    rc = L.mx_attn_decode(cache.cfg.ref(), ref, q.data_ptr(), _DT[q.dtype], ldq, S, Hq, page_table.data_ptr(), ldt, pages, pl,
+                          D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _DT[out.dtype], ldo,
+                          _p(ls), _p(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
+    if rc:
+        _check("mx_attn_decode", rc)
     return (out, ls) if lse else out
 
 
