@@ -7,58 +7,55 @@
 //   blocks as mx_quantize writes them, bit for bit.
 //
 // Bound: every input read and every output written once (HBM bandwidth) for
-// many tokens, latency for a few.  Eight consecutive elements a lane (16-byte
-// bf16 loads): D / 8 lanes hold a head, a rotation partner D' / 2 elements
-// away is the same register of another lane (D' / 2 a multiple of 8) or, in
-// neighbouring pairs, in the lane itself; a block is block / 8 lanes, so norm,
-// partner and block maximum are shuffles and nothing goes through shared
-// memory but the angles.  A token's angles serve all its heads: position
-// times inv_freq / 2 pi in binary64, reduced to a fraction of a turn there
-// (exact to 2^-53 turns per turn at any position), then one sincospi each,
-// computed once per token and CTA.
+// many tokens, latency for a few.  A warp takes a token, or a share of its
+// heads when tokens are few, and goes over query, key and value heads in
+// turn.  Eight consecutive elements a lane (16-byte bf16 loads): D / 8 lanes
+// hold a head, a rotation partner D' / 2 elements away is the same register of
+// another lane (D' / 2 a multiple of 8) or, in neighbouring pairs, in the lane
+// itself; a block is block / 8 lanes, so norm, partner and block maximum are
+// shuffles.  A token's angles serve all its heads and stay in registers, as do
+// the gains.  Each lane copies its own pieces of the coming heads into a ring
+// in shared memory (seven 512-byte loads of a warp in flight).  Angles:
+// position times inv_freq / 2 pi in binary64, reduced to a fraction of a turn
+// there (2^-53 of the turns), then one sincospi, shared by the warp.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "mma_decode.cuh"
 #include "mx_internal.h"
 
 namespace mxk {
 
 constexpr int kKvThreads = 256;
 constexpr int kKvWarps = kKvThreads / 32;
+constexpr int kKvRing = 4096;   // bytes of a warp's ring
 
 // elements of the quantized rows: conversion instructions, or the general rounding
 enum { KE_E2M1 = 0, KE_E2M3 = 1, KE_E3M2 = 2, KE_ANY = 3 };
 // block scales: powers of two in E8M0, nearest unsigned minifloat, powers of two in one
 enum { KS_E8M0 = 0, KS_NEAR = 1, KS_POW2 = 2 };
 
-template <bool FP32> __device__ __forceinline__ void kv_load8(const void *base, int64_t at, bool vec, float v[8])
+// Eight values of a row as loaded, and in binary32.
+template <bool FP32> struct KvRaw { uint32_t w[FP32 ? 8 : 4]; };
+
+template <bool FP32> __device__ __forceinline__ void kv_load8(const void *src, KvRaw<FP32> &r)
 {
     if (FP32) {
-        const float *x = static_cast<const float *>(base) + at;
-        if (vec) {
-            const float4 a = *reinterpret_cast<const float4 *>(x), b = *reinterpret_cast<const float4 *>(x + 4);
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-        } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = x[i];
-        }
+        for (int i = 0; i < 8; ++i) r.w[FP32 ? i : 0] = static_cast<const uint32_t *>(src)[i];
     } else {
-        const uint16_t *x = static_cast<const uint16_t *>(base) + at;
-        uint32_t w[4];
-        if (vec) {
-            const uint4 a = *reinterpret_cast<const uint4 *>(x);
-            w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        } else {
+        const uint16_t *x = static_cast<const uint16_t *>(src);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
-        }
+        for (int i = 0; i < 4; ++i) r.w[i] = x[2 * i] | ((uint32_t)x[2 * i + 1] << 16);
+    }
+}
+template <bool FP32> __device__ __forceinline__ void kv_values(const KvRaw<FP32> &r, float v[8])
+{
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = bits2f(w[i] << 16);
-            v[2 * i + 1] = bits2f(w[i] & 0xffff0000u);
-        }
+    for (int i = 0; i < 4; ++i) {
+        v[2 * i] = FP32 ? bits2f(r.w[FP32 ? 2 * i : 0]) : bits2f(r.w[i] << 16);
+        v[2 * i + 1] = FP32 ? bits2f(r.w[FP32 ? 2 * i + 1 : 0]) : bits2f(r.w[i] & 0xffff0000u);
     }
 }
 
@@ -99,7 +96,7 @@ template <bool FP32> __device__ __forceinline__ void kv_round_store8(void *base,
 // store codes and scale; every lane of the warp takes part in the shuffles.
 template <int EK, int SK>
 __device__ __forceinline__ void kv_quantize8(const KvAppendParams &p, const NearScale &ns, const float v[8], bool store,
-                                             uint8_t *codes, uint8_t *scales, int64_t row, int col)
+                                             uint8_t *codes, uint8_t *scales, int64_t at)
 {
     uint32_t m = 0;
 #pragma unroll
@@ -115,7 +112,6 @@ __device__ __forceinline__ void kv_quantize8(const KvAppendParams &p, const Near
     float s[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) s[i] = __fmul_rn(v[i], bs.inv);
-    const int64_t at = row * p.cols + col;
     if (EK == KE_E2M1) {
         *reinterpret_cast<uint32_t *>(codes + (at >> 1)) = bs.zero ? 0u : cvt_e2m1x8(s);
     } else if (EK == KE_E2M3 || EK == KE_E3M2) {
@@ -149,120 +145,225 @@ __device__ __forceinline__ void kv_quantize8(const KvAppendParams &p, const Near
 }
 
 template <int D, bool FP32, int EK, int SK>
-__global__ void __launch_bounds__(kKvThreads) k_kv_append(const __grid_constant__ KvAppendParams p)
+__global__ void __launch_bounds__(kKvThreads, 3) k_kv_append(const __grid_constant__ KvAppendParams p)
 {
-    constexpr int L = D / 8, RPW = 32 / L;      // lanes of a head, heads of a warp
-    extern __shared__ float2 cs[];              // cos, sin: [tokens of a group][rot / 2]
+    constexpr int L = D / 8, RPW = 32 / L;            // lanes of a head, heads of a warp
+    __shared__ float2 cs_all[kKvWarps][D / 2];        // cos, sin of a warp's token
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int l = lane & (L - 1), sub = lane / L;
     const int half = p.rot >> 1;
+    float2 *cs = cs_all[warp];
     pdl_trigger();
     pdl_wait();
 
     // nearest scales: the scale and its reciprocal for every code, of keys and of values
     __shared__ float2 tab[SK == KS_NEAR ? 512 : 1];
-    NearScale ns[2];   // (indexed by constants only)
+    NearScale ns_k, ns_v;
     if (SK == KS_NEAR) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float *ts = i ? p.v_ts : p.k_ts;
+        const auto make = [&](NearScale &ns, const float *ts, float2 *t) {
             const float sT = ts ? *ts : 1.0f;
             for (int c = threadIdx.x; c < 256; c += kKvThreads) {
                 const float d = __fmul_rn(ue_value(p.sd, (uint32_t)c), sT);
-                tab[256 * i + c] = c < p.sd.ue_nan_code ? make_float2(d, __fdiv_rn(1.0f, d)) : make_float2(bits2f(0x7fc00000u), 0.0f);
+                t[c] = c < p.sd.ue_nan_code ? make_float2(d, __fdiv_rn(1.0f, d)) : make_float2(bits2f(0x7fc00000u), 0.0f);
             }
-            ns[i].maxv = p.ed.maxv;
-            ns[i].r_max = __fdiv_rn(1.0f, p.ed.maxv);
-            ns[i].sT = sT;
-            ns[i].r_T = (sT >= 0x1p-125f && sT <= 0x1p125f) ? __fdiv_rn(1.0f, sT) : 0.0f;
+            ns.maxv = p.ed.maxv;
+            ns.r_max = __fdiv_rn(1.0f, p.ed.maxv);
+            ns.sT = sT;
+            ns.r_T = (sT >= 0x1p-125f && sT <= 0x1p125f) ? __fdiv_rn(1.0f, sT) : 0.0f;
             const float ms = __fmul_rn(p.ed.maxv, sT);
-            ns[i].c = (ms >= 0x1p-125f && ms <= 0x1p125f) ? __fdiv_rn(1.0f, ms) : 0.0f;
-            ns[i].tab = tab + 256 * i;
-        }
+            ns.c = (ms >= 0x1p-125f && ms <= 0x1p125f) ? __fdiv_rn(1.0f, ms) : 0.0f;
+            ns.tab = t;
+        };
+        make(ns_k, p.k_ts, tab);
+        make(ns_v, p.v_ts, tab + (SK == KS_NEAR ? 256 : 0));
+        __syncthreads();
     }
 
-    const int rows = p.q_heads + 2 * p.kv_heads;   // heads of a token: queries, keys, values
-    const int per_y = (rows + gridDim.y - 1) / gridDim.y;
-    const int r0 = blockIdx.y * per_y, rn = min(per_y, rows - r0);
-    for (int64_t t0 = (int64_t)blockIdx.x * p.group; t0 < p.tokens; t0 += (int64_t)gridDim.x * p.group) {
-        const int tn = (int)min((int64_t)p.group, p.tokens - t0);
-        __syncthreads();   // the last group's angles are no longer read
-        for (int i = threadIdx.x; i < tn * half; i += kKvThreads) {
-            const int tk = i / half;
-            const double turns = (double)p.positions[t0 + tk] * ((double)p.inv_freq[i - tk * half] * 0.15915494309189533577);
-            float sn, cn;
-            sincospif(2.0f * (float)(turns - rint(turns)), &sn, &cn);
-            cs[i] = make_float2(cn, sn);
+    const bool turns = 8 * l < p.rot;                 // the lane's elements are rotated
+    const int dl = p.rot >> 4;                        // lanes to the partner (pairs rot / 2 apart)
+    const bool lo = l < dl;
+    const int from = (lane & ~(L - 1)) | ((lo ? l + dl : l - dl) & (L - 1));
+
+    // a token's heads in units of RPW: queries, keys, values
+    const int nq = (p.q_heads + RPW - 1) / RPW, nk = (p.kv_heads + RPW - 1) / RPW, units = nq + 2 * nk;
+    const int64_t tasks = p.tokens * p.parts, stride = (int64_t)gridDim.x * kKvWarps;
+    const int64_t first = (int64_t)blockIdx.x * kKvWarps + warp;
+
+    // where a lane's eight values of a unit are
+    constexpr int ES = FP32 ? 4 : 2;
+    const auto source = [&](int64_t tok, int u) {
+        const char *src;
+        int64_t ld;
+        int h0;
+        if (u < nq) src = static_cast<const char *>(p.q), ld = p.ldq, h0 = u;
+        else if (u < nq + nk) src = static_cast<const char *>(p.k), ld = p.ldk, h0 = u - nq;
+        else src = static_cast<const char *>(p.v), ld = p.ldv, h0 = u - nq - nk;
+        return src + (tok * ld + (h0 * RPW + sub) * D + 8 * l) * ES;
+    };
+    // (the last unit of a kind may have fewer heads than the warp has room for)
+    const auto present = [&](int u) {
+        const int h = (u < nq ? u : u < nq + nk ? u - nq : u - nq - nk) * RPW + sub;
+        return h < (u < nq ? p.q_heads : p.kv_heads);
+    };
+    // the lane's ring: pieces of the units to come, this task's and the next
+    constexpr int PIECE = FP32 ? 32 : 16, STAGES = kKvRing / (32 * PIECE);
+    extern __shared__ __align__(16) uint8_t ring_all[];
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(ring_all) + warp * kKvRing + lane * 16;
+    const uint32_t ring_end = ring + STAGES * 32 * PIECE;
+    const auto span = [&](int64_t task, int64_t &tok, int &u0, int &u1) {
+        if (p.parts == 1) {
+            tok = task;
+            u0 = 0;
+            u1 = units;
+        } else {
+            tok = task / p.parts;
+            const int part = (int)(task - tok * p.parts);
+            u0 = units * part / p.parts;
+            u1 = units * (part + 1) / p.parts;
         }
-        __syncthreads();
-        const int items = tn * rn;
-        for (int i0 = warp * RPW; i0 < items; i0 += kKvWarps * RPW) {
-            const int i = min(i0 + sub, items - 1);
-            const bool on = i0 + sub < items;
-            const int tk = i / rn, r = r0 + i - tk * rn;
-            const int64_t tok = t0 + tk;
-            const int kind = r < p.q_heads ? 0 : r < p.q_heads + p.kv_heads ? 1 : 2;
-            const int head = r - (kind == 0 ? 0 : kind == 1 ? p.q_heads : p.q_heads + p.kv_heads);
-            const void *src = kind == 0 ? p.q : kind == 1 ? p.k : p.v;
-            const int64_t ld = kind == 0 ? p.ldq : kind == 1 ? p.ldk : p.ldv;
-            float v[8];
-            kv_load8<FP32>(src, tok * ld + head * D + 8 * l, p.in_vec, v);
-            const float *gain = kind == 0 ? p.q_gain : kind == 1 ? p.k_gain : nullptr;
-            if (p.q_gain || p.k_gain) {
+    };
+    int64_t ahead = first, atok = 0;
+    int au = 0, aend = 0;
+    const char *asrc = nullptr;
+    uint32_t st_w = ring, st_r = ring;
+    const auto issue = [&]() {
+        if (ahead < tasks) {
+            const bool in = present(au);
+            const char *src = in ? asrc : static_cast<const char *>(p.k);
+            cp_async16(st_w, src, in ? 16 : 0);
+            if (FP32) cp_async16(st_w + 512, in ? src + 16 : src, in ? 16 : 0);
+            ++au;
+            asrc += RPW * D * ES;
+            if (au == aend) {
+                ahead += stride;
+                if (ahead < tasks) {
+                    span(ahead, atok, au, aend);
+                    asrc = source(atok, au);
+                }
+            } else if (au == nq || au == nq + nk) {
+                asrc = source(atok, au);
+            }
+        }
+        cp_async_commit();
+        st_w = st_w + 32 * PIECE == ring_end ? ring : st_w + 32 * PIECE;
+    };
+    if (p.in_vec && first < tasks) {
+        span(first, atok, au, aend);
+        asrc = source(atok, au);
+        for (int i = 0; i < STAGES - 1; ++i) issue();
+    }
+
+    for (int64_t task = first; task < tasks; task += stride) {
+        int64_t tok;
+        int u0, u1;
+        span(task, tok, u0, u1);
+        const int64_t slot = p.slots[tok];
+        const bool stored = slot >= 0 && slot < p.cache_rows;
+        float2 c[8];
+        if (half && u0 < nq + nk) {
+            const double pos = (double)p.positions[tok];
+            __syncwarp();                             // the last token's angles are read
+            for (int i = lane; i < half; i += 32) {
+                const double t = pos * ((double)p.inv_freq[i] * 0.15915494309189533577);
+                float sn, cn;
+                sincospif(2.0f * (float)(t - rint(t)), &sn, &cn);
+                cs[i] = make_float2(cn, sn);
+            }
+            __syncwarp();
+            if (turns) {
+                // (a cos - b sin, b cos + a sin): the sine of the first of a
+                // pair with its sign
+                const int at = p.interleaved ? 4 * l : 8 * (lo ? l : l - dl);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    c[j] = cs[at + (p.interleaved ? j >> 1 : j)];
+                    if (p.interleaved ? (j & 1) == 0 : lo) c[j].y = -c[j].y;
+                }
+            }
+        }
+        const auto take = [&](int u, float v[8]) {
+            KvRaw<FP32> raw;
+            if (p.in_vec) {
+                cp_async_wait<STAGES - 2>();
+                const uint4 x = lds128(st_r);
+                raw.w[0] = x.x; raw.w[1] = x.y; raw.w[2] = x.z; raw.w[3] = x.w;
+                if (FP32) {
+                    const uint4 y = lds128(st_r + 512);
+                    raw.w[FP32 ? 4 : 0] = y.x; raw.w[FP32 ? 5 : 0] = y.y; raw.w[FP32 ? 6 : 0] = y.z; raw.w[FP32 ? 7 : 0] = y.w;
+                }
+                st_r = st_r + 32 * PIECE == ring_end ? ring : st_r + 32 * PIECE;
+                issue();
+            } else {
+                kv_load8<FP32>(present(u) ? source(tok, u) : static_cast<const char *>(p.k), raw);
+            }
+            kv_values<FP32>(raw, v);
+        };
+        // norm and rotation of queries or keys
+        const auto turn = [&](const float *gain, const float g[8], float v[8]) {
+            if (gain) {
                 float ss = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) ss = fmaf(v[j], v[j], ss);
 #pragma unroll
                 for (int d = L / 2; d; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-                if (gain) {
-                    const float f = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), p.eps));
-                    const float4 a = *reinterpret_cast<const float4 *>(gain + 8 * l), b = *reinterpret_cast<const float4 *>(gain + 8 * l + 4);
-                    const float g[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+                const float f = rsqrtf(__fadd_rn(__fmul_rn(ss, 1.0f / D), p.eps));
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], f), g[j]);
-                }
+                for (int j = 0; j < 8; ++j) v[j] = __fmul_rn(__fmul_rn(v[j], f), g[j]);
             }
-            if (p.rot) {
+            if (half) {
+                float o[8];
                 if (p.interleaved) {
-                    if (kind < 2 && 8 * l < p.rot) {
-                        const float2 *c = cs + tk * half + 4 * l;
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float a = v[2 * j], b = v[2 * j + 1];
-                            v[2 * j] = fmaf(a, c[j].x, -__fmul_rn(b, c[j].y));
-                            v[2 * j + 1] = fmaf(b, c[j].x, __fmul_rn(a, c[j].y));
-                        }
-                    }
+                    for (int j = 0; j < 8; ++j) o[j] = v[j ^ 1];
                 } else {
-                    // element i of the first half pairs with i + rot / 2: the
-                    // same register rot / 16 lanes on
-                    const int dl = p.rot >> 4;
-                    const bool lo = l < dl;
-                    const int from = (lane & ~(L - 1)) | ((lo ? l + dl : l - dl) & (L - 1));
-                    float o[8];
 #pragma unroll
                     for (int j = 0; j < 8; ++j) o[j] = __shfl_sync(0xffffffffu, v[j], from);
-                    if (kind < 2 && 8 * l < p.rot) {
-                        const float2 *c = cs + tk * half + 8 * (lo ? l : l - dl);
+                }
+                if (turns) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float t = __fmul_rn(o[j], c[j].y);
-                            v[j] = fmaf(v[j], c[j].x, lo ? -t : t);
-                        }
-                    }
+                    for (int j = 0; j < 8; ++j) v[j] = fmaf(v[j], c[j].x, __fmul_rn(o[j], c[j].y));
                 }
             }
-            if (kind == 0) kv_round_store8<FP32>(p.q_out, tok * p.ldqo + head * D + 8 * l, p.out_vec, on, v);
-            else kv_round_store8<FP32>(p.k_out, tok * p.ldko + head * D + 8 * l, p.out_vec, on && kind == 1 && p.k_out, v);
-            const int64_t slot = p.slots[tok];
-            const bool store = on && kind != 0 && slot >= 0 && slot < p.cache_rows;
-            if (__any_sync(0xffffffffu, store))
-            {
-                NearScale n = ns[0];
-                if (SK == KS_NEAR && kind == 2) n = ns[1];
-                kv_quantize8<EK, SK>(p, n, v, store, kind == 1 ? p.k_codes : p.v_codes,
-                                     kind == 1 ? p.k_scales : p.v_scales, slot, head * D + 8 * l);
+        };
+        const auto gains = [&](const float *gain, float g[8]) {
+            if (!gain) return;
+            const float4 a = *reinterpret_cast<const float4 *>(gain + 8 * l), b = *reinterpret_cast<const float4 *>(gain + 8 * l + 4);
+            g[0] = a.x; g[1] = a.y; g[2] = a.z; g[3] = a.w;
+            g[4] = b.x; g[5] = b.y; g[6] = b.z; g[7] = b.w;
+        };
+        const int64_t row = stored ? slot * p.cols : 0;
+        int u = u0;
+        if (u < nq) {
+            float g[8];
+            gains(p.q_gain, g);
+            const int64_t out = tok * p.ldqo + 8 * l;
+            for (const int e = min(u1, nq); u < e; ++u) {
+                float v[8];
+                take(u, v);
+                turn(p.q_gain, g, v);
+                const int head = u * RPW + sub;
+                kv_round_store8<FP32>(p.q_out, out + head * D, p.out_vec, head < p.q_heads, v);
             }
+        }
+        if (u < u1 && u < nq + nk) {
+            float g[8];
+            gains(p.k_gain, g);
+            const int64_t out = tok * p.ldko + 8 * l;
+            for (const int e = min(u1, nq + nk); u < e; ++u) {
+                float v[8];
+                take(u, v);
+                turn(p.k_gain, g, v);
+                const int head = (u - nq) * RPW + sub;
+                const bool on = head < p.kv_heads;
+                kv_round_store8<FP32>(p.k_out, out + head * D, p.out_vec, on && p.k_out, v);
+                kv_quantize8<EK, SK>(p, ns_k, v, on && stored, p.k_codes, p.k_scales, row + head * D + 8 * l);
+            }
+        }
+        for (; u < u1; ++u) {
+            float v[8];
+            take(u, v);
+            const int head = (u - nq - nk) * RPW + sub;
+            kv_quantize8<EK, SK>(p, ns_v, v, head < p.kv_heads && stored, p.v_codes, p.v_scales, row + head * D + 8 * l);
         }
     }
 }
@@ -299,27 +400,16 @@ int launch_kv_append(KvAppendParams p, int head_dim, int in_fp32, cudaStream_t s
     const int sk = p.sd.fmt == S_E8M0 ? KS_E8M0 : p.sd.rule == R_NEAREST ? KS_NEAR : KS_POW2;
     KvKernel k = head_dim == 64 ? kv_pick_type<64>(in_fp32, ek, sk) : head_dim == 128 ? kv_pick_type<128>(in_fp32, ek, sk)
                                                                     : kv_pick_type<256>(in_fp32, ek, sk);
-    // few tokens: one a CTA, its heads over several CTAs (a warp's worth of
-    // work each); many: groups of four, whose angles one barrier covers
-    const int rows = p.q_heads + 2 * p.kv_heads, pass = kKvWarps * (256 / head_dim);
-    const int64_t slots = 4 * (int64_t)device_sm_count();
-    p.group = p.tokens > 4 * slots ? 4 : 1;
-    const int64_t groups = (p.tokens + p.group - 1) / p.group;
-    int64_t y = (rows + pass - 1) / pass;
-    if (groups * y > slots) y = slots / groups > 1 ? slots / groups : 1;
-    const int64_t x = groups < slots ? groups : slots;
-    const size_t smem = (size_t)p.group * (p.rot / 2) * sizeof(float2);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)x, (unsigned)y);
-    cfg.blockDim = dim3(kKvThreads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, k, p) == cudaSuccess ? 0 : 1;
+    // few tokens: a token's heads over as many warps as the device holds, one
+    // unit each at the least; many: a warp a token
+    const int rpw = 256 / head_dim;
+    const int64_t units = (p.q_heads + rpw - 1) / rpw + 2 * ((p.kv_heads + rpw - 1) / rpw);
+    const int64_t warps = (int64_t)device_sm_count() * 3 * kKvWarps;
+    int64_t parts = warps / p.tokens;
+    parts = parts < 1 ? 1 : parts > units ? units : parts;
+    p.parts = (int)parts;
+    const int64_t ctas = (p.tokens * parts + kKvWarps - 1) / kKvWarps, most = 16 * (int64_t)device_sm_count();
+    return launch_pdl(k, (unsigned)(ctas < most ? ctas : most), kKvThreads, kKvWarps * kKvRing, st, p) == cudaSuccess ? 0 : 1;
 }
 
 }  // namespace mxk

@@ -119,7 +119,7 @@ struct KvAppendParams {
     ScaleDesc sd;
     int round_mode, lanes_per_block, log2B;
     float thr_m;             // e8m0_threshold of the rule
-    int group;               // tokens whose angles a CTA holds (set by the launch)
+    int parts;               // warps that share a token's heads (set by the launch)
 };
 
 // Most stretches an mx_attn_decode call splits a sequence into
