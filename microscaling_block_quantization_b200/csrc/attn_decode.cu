@@ -96,18 +96,19 @@ AtPick at_pick(int el, int d, int bs, int nth, int hp)
 
 }  // namespace
 
-// Splits of every sequence for a call of these sizes: enough warps to fill
-// the device about twice (ragged sequences even out), stretches of 128 tokens
-// at least.
+// Splits of every sequence for a call of these sizes.  The device holds about
+// 16 of the warps an SM: one sequence is split into as many stretches as run at
+// once; several, whose lengths differ, into twice as many, so that a warp
+// that is done makes room for another.  Stretches of 64 tokens at least.
 int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens)
 {
     const int group = q_heads / kv_heads;
     const int hg = group <= 4 ? 1 : (group + 7) / 8;
     const int64_t rows = seqs * kv_heads * hg;
     if (rows <= 0) return 1;
-    const int64_t want = (int64_t)device_sm_count() * 32;
+    const int64_t want = (int64_t)device_sm_count() * (seqs == 1 ? 16 : 32);
     int64_t s = want / rows;
-    const int64_t cap = (most_tokens + 127) / 128;
+    const int64_t cap = (most_tokens + 63) / 64;
     s = s < cap ? s : cap;
     return s < 1 ? 1 : s > kAttnMaxSplits ? kAttnMaxSplits : (int)s;
 }

@@ -265,7 +265,7 @@ __device__ __forceinline__ void at_visible(const AttnParams &p, int b, int &n, i
 // NTH: groups of four heads (1 or 2); HP: binary32 precision (two pieces of
 // queries and weights)
 template <int EL, int D, int BS, int NTH, int HP>
-__global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4) k_attn(const __grid_constant__ AttnParams p)
 {
     using G = AtGeom<EL, D, BS>;
     constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
@@ -300,33 +300,45 @@ __global__ void __launch_bounds__(kAtThreads) k_attn(const __grid_constant__ Att
     // lanes 0..15 copy key scales of their token, 16..31 value scales
     const uint8_t *sc = (lane < 16 ? p.k_scales : p.v_scales) + (G::NARROW ? 0 : kh * nsc);
 
-    // page number of the lane's token (lane & 15) in a tile; -1 behind the end
-    auto page_of = [&](int tile, int &off) {
-        const int i = tile * 16 + (lane & 15);
-        if (tile >= tile1 || i >= vis) return -1;
+    // Rows are looked up for two tiles at a time, a token a lane: the page
+    // number of a lane's token is loaded two tiles before its row is used.
+    const auto page_of = [&](int tile, int &off) {
+        const int i = tile * 16 + lane;
+        if (i >= vis || (lane >= 16 && tile + 1 >= tile1)) return -1;
         const int tok = i < sinks ? i : i + skip;
         const int pg = p.page_shift >= 0 ? tok >> p.page_shift : tok / p.page_size;
         off = tok - pg * p.page_size;
         return (int)table[pg];
     };
-    int next_off = 0, next_page = page_of(tile0, next_off), it = tile0;
+    int next_off = 0, next_page = tile0 < tile1 ? page_of(tile0, next_off) : -1, it = tile0;
+    uint32_t rows = 0u, there = 0u;           // of the two tiles: the lane's row, the tokens that are there
     uint32_t st_w = ring;
-    auto issue = [&]() {
+    constexpr int RPI = 32 / G::NPC;          // rows of one round of copies (NPC <= 32)
+    const uint32_t pr = lane / G::NPC, pc = lane % G::NPC;
+    kc += pc * 16;
+    vc += pc * 16;
+    const auto issue = [&]() {
         if (it < tile1) {
-            const bool ok = (uint32_t)next_page < (uint32_t)p.pages;
-            const uint32_t row = ok ? (uint32_t)(next_page * p.page_size + next_off) : 0u;
-            const uint32_t mask = __ballot_sync(0xffffffffu, ok) & 0xffffu;   // the tokens that are there
+            const int second = (it - tile0) & 1;
+            if (!second) {
+                const bool ok = (uint32_t)next_page < (uint32_t)p.pages;
+                rows = ok ? (uint32_t)(next_page * p.page_size + next_off) : 0u;
+                there = __ballot_sync(0xffffffffu, ok);
+                if (it + 2 < tile1) next_page = page_of(it + 2, next_off);
+            }
+            const uint32_t mask = second ? there >> 16 : there & 0xffffu;
             ++it;
-            next_page = page_of(it, next_off);
 #pragma unroll
-            for (int i = 0; i < G::NPC / 2; ++i) {
-                const int idx = i * 32 + lane, r = idx / G::NPC, pc = idx % G::NPC;
-                const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, row, r) * code_row + pc * 16;
+            for (int i = 0; i < 16 / RPI; ++i) {
+                const int r = i * RPI + pr;
+                const uint64_t at = (uint64_t)__shfl_sync(0xffffffffu, rows, r + 16 * second) * code_row;
                 const int nb = (mask >> r) & 1 ? 16 : 0;
                 const uint32_t dst = st_w + r * G::ROW + ((pc ^ G::swz(r)) << 4);
                 cp_async16(dst + G::K_AT, kc + at, nb);
                 cp_async16(dst + G::V_AT, vc + at, nb);
             }
+            const uint32_t row = __shfl_sync(0xffffffffu, rows, (lane & 15) + 16 * second);
+            const bool ok = (mask >> (lane & 15)) & 1;
             const uint32_t dst = st_w + (lane < 16 ? G::KS_AT : G::VS_AT) + (lane & 15) * G::SW;
             if (!G::NARROW) {
                 // (BS 32: a byte per 32-block, BS 16: two)
