@@ -260,7 +260,7 @@ __device__ __forceinline__ float2 gv_pair(const GvRaw<true> &r, int i) { return 
 // x chunks [c0, c0 + n) of the token group as f16 pieces in the order the
 // matrix instruction's lanes read them: 16 lanes per (chunk, token), 8
 // consecutive values each.
-template <int BC, int NT, bool FP32>
+template <int BC, int NT, bool FP32, bool SPREAD, bool GROUP>
 __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, int64_t tok0, int toks, int c0, int n)
 {
     const int l = threadIdx.x & 15, half = (threadIdx.x >> 4) & 1;
@@ -294,6 +294,10 @@ __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, i
                 }
                 sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 1));
                 sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 2));
+                if (GROUP) {
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 4));
+                    sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, 8));
+                }
             }
             if (it >= items) continue;
             const int e = f16_scale_exponent(bits2f(m));
@@ -320,7 +324,12 @@ __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, i
             for (int pc = 0; pc < P; ++pc) {
                 const int col = tok * P + pc;
                 uint8_t *dst = smem + gm.xs_at + (((c * 4 + (l >> 2)) * NT + (col >> 3)) << 9) + (col & 7) * 64;
-                if (BC == 32) {
+                if (SPREAD) {
+                    // pairs (i, i + 4), as int4_halves_spread leaves them
+                    *reinterpret_cast<uint4 *>(dst + q * 16) =
+                        make_uint4(__byte_perm(h[pc][0], h[pc][2], 0x5410u), __byte_perm(h[pc][0], h[pc][2], 0x7632u),
+                                   __byte_perm(h[pc][1], h[pc][3], 0x5410u), __byte_perm(h[pc][1], h[pc][3], 0x7632u));
+                } else if (BC == 32) {
                     *reinterpret_cast<uint4 *>(dst + q * 16) = make_uint4(h[pc][0], h[pc][1], h[pc][2], h[pc][3]);
                 } else if (BC == 16) {
                     const int t = 2 * (q & 1), o = (q >> 1) * 8;
@@ -331,11 +340,18 @@ __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, i
                     for (int i = 0; i < 4; ++i) *reinterpret_cast<uint32_t *>(dst + i * 16 + q * 4) = h[pc][i];
                 }
                 if (l == 0) ex[c * 8 * NT + col] = exp2i(-e - 11 * pc);
-                if (p.off && q == 0) xsum[(c * 4 + (l >> 2)) * 8 * NT + col] = pc ? 0.0f : sum;
+                if (p.off && GROUP) {
+                    if (l == 0) xsum[c * 8 * NT + col] = pc ? 0.0f : sum;
+                } else if (p.off && q == 0) {
+                    xsum[(c * 4 + (l >> 2)) * 8 * NT + col] = pc ? 0.0f : sum;
+                }
             }
         }
     }
 }
+
+// INT4 words whose eight codes share a block are decoded in pairs (i, i + 4)
+template <int ELEM, int BC> __host__ __device__ constexpr bool gv_spread() { return BC == 32 && (ELEM == GE_INT4 || ELEM == GE_UINT4); }
 
 // One unit of a warp: acc += (16 rows x 128 columns of codes in the stage) x
 // (chunk cx of the staged x).
@@ -371,8 +387,13 @@ __device__ __forceinline__ void gv_unit(const GvParams &p, uint32_t st, uint32_t
             wh = __byte_perm(__byte_perm(x1.x, x1.y, sel), __byte_perm(x1.z, x1.w, sel), 0x5410u);
         }
         uint32_t hl[4], hh[4];
-        codes8_halves<ELEM>(wl, hl);
-        codes8_halves<ELEM>(wh, hh);
+        if constexpr (gv_spread<ELEM, BC>()) {
+            int4_halves_spread<ELEM>(wl, hl);
+            int4_halves_spread<ELEM>(wh, hh);
+        } else {
+            codes8_halves<ELEM>(wl, hl);
+            codes8_halves<ELEM>(wh, hh);
+        }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const uint4 xb = lds128(xs + ((b * NT + n) << 9) + lane * 16);
@@ -438,15 +459,7 @@ __device__ __forceinline__ void gv_unit(const GvParams &p, uint32_t st, uint32_t
         const float fl = bits2f(lds16(ol + j) << 16), fh = bits2f(lds16(oh + j) << 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float2 v = *reinterpret_cast<const float2 *>(xsum + (b * NT + n) * 8 + 2 * t);
-            if (MODE == GM_GROUP) {
-#pragma unroll
-                for (int k = 1; k < 4; ++k) {
-                    const float2 u = *reinterpret_cast<const float2 *>(xsum + (k * NT + n) * 8 + 2 * t);
-                    v.x = __fadd_rn(v.x, u.x);
-                    v.y = __fadd_rn(v.y, u.y);
-                }
-            }
+            const float2 v = *reinterpret_cast<const float2 *>(xsum + (b * NT + n) * 8 + 2 * t);
             acc[n][0] = fmaf(fl, v.x, acc[n][0]);
             acc[n][1] = fmaf(fl, v.y, acc[n][1]);
             acc[n][2] = fmaf(fh, v.x, acc[n][2]);
@@ -462,6 +475,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
     extern __shared__ __align__(128) uint8_t smem[];
     cg::cluster_group cluster = cg::this_cluster();
     constexpr int SB = gv_stage_bytes<MODE, BC>();
+    constexpr bool SPREAD = gv_spread<ELEM, BC>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
     const int rank = (int)(blockIdx.x % gm.C);
@@ -508,8 +522,8 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
             for (int i = 0; i < kGvStages - 1; ++i) issue();
             if (!resident || w0 == 0) {
                 if (s0 != c_lo || w0 != 0) __syncthreads();   // the last slice of x is no longer read
-                if (p.x_fp32) gv_stage_x<BC, NT, true>(p, gm, smem, tok0, toks, s0, sn);
-                else gv_stage_x<BC, NT, false>(p, gm, smem, tok0, toks, s0, sn);
+                if (p.x_fp32) gv_stage_x<BC, NT, true, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0, sn);
+                else gv_stage_x<BC, NT, false, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0, sn);
                 __syncthreads();
             }
             uint32_t st = ring;
@@ -529,7 +543,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
                     __syncwarp();   // every lane's copies of this unit are in, and the last unit is read
                     issue();
                     gv_unit<ELEM, MODE, BC, NT>(p, st, sbase + gm.xs_at + cx * (NT << 11), ex + cx * NT * 8,
-                                                xsum + cx * NT * 32, a_lo, a_hi, m_lo, m_hi, a + c, lane, acc);
+                                                xsum + cx * NT * (MODE == GM_GROUP ? 8 : 32), a_lo, a_hi, m_lo, m_hi, a + c, lane, acc);
                     st = st + SB == ring_end ? ring : st + SB;
                 }
                 // this warp's partial sums of the tile: 16 rows of each

@@ -57,6 +57,24 @@ __device__ __forceinline__ void codes8_halves(uint32_t w, uint32_t h[4])
     }
 }
 
+// Eight INT4 codes of a word -> four f16x2 with codes (i, i + 4) in h[i]: the
+// nibbles of a half word where they stand, under the exponent of 1024 (an f16
+// ulp is 1: 1024 + n, or 1024 + 16 n four bits up), then the constant off:
+// half the integer operations of neighbouring pairs.
+template <int ELEM>
+__device__ __forceinline__ void int4_halves_spread(uint32_t w, uint32_t h[4])
+{
+    constexpr uint32_t F = ELEM == GE_INT4 ? 0x8u : 0x0u;   // two's complement: flip the sign bit, take 8 off
+    const uint32_t lo = 0x64006400u | F | (F << 16), hi = 0x64006400u | (F << 4) | (F << 20);
+    const uint32_t off = ELEM == GE_INT4 ? 0xe408e408u : 0xe400e400u;       // -(1024 + 8), -1024
+    const uint32_t off16 = ELEM == GE_INT4 ? 0xd480d480u : 0xd400d400u;     // -(64 + 8), -64
+    const uint32_t v = w >> 8;
+    h[0] = hadd2_u((w & 0x000f000fu) ^ lo, off);
+    h[2] = hadd2_u((v & 0x000f000fu) ^ lo, off);
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[1]) : "r"((w & 0x00f000f0u) ^ hi), "r"(0x2c002c00u), "r"(off16));   // / 16
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(h[3]) : "r"((v & 0x00f000f0u) ^ hi), "r"(0x2c002c00u), "r"(off16));
+}
+
 // A block-scale code -> binary32.  Unsigned minifloats with 3 mantissa bits:
 // the byte shifted into an exponent and mantissa, rescaled by an exact power
 // of two.
