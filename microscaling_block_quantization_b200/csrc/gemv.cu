@@ -69,42 +69,45 @@ int launch_gemv(GvParams p, cudaStream_t st)
     const int P = p.x_fp32 ? 2 : 1;
     const int nt = p.M * P > 8 ? 2 : 1;
     p.group = 8 * nt / P;
-    p.chunks = (int)((p.K + 127) / 128);
     const int64_t tiles = (p.N + 15) / 16;
 
+    const bool wide = p.K % 256 == 0 && !p.macro;
+    const int mode = wide && p.log2B >= 7 ? GM_GROUP : wide && p.log2B <= 5 && !p.off ? GM_BLOCK : GM_ANY;
+    const int uc = gv_chunks(mode);
+    p.units = (int)((p.K + 128 * uc - 1) / (128 * uc));
     GvGeom gm = {};
-    const int mode = p.log2B >= 7 && !p.macro ? GM_GROUP
-                   : p.log2B <= 5 && p.K % 128 == 0 && !p.macro && !p.off ? GM_BLOCK : GM_ANY;
     const int stage = mode == GM_GROUP ? gv_stage_bytes<GM_GROUP, 32>()
                     : mode == GM_BLOCK ? gv_stage_size<GM_BLOCK>(bc) : gv_stage_size<GM_ANY>(bc);
-    const int ring = kGvWarps * kGvStages * stage;
+    const int ring = kGvWarps * gv_stages(mode) * stage;
     const int x_room = kGvSmem - ring - 32 * 1024;   // x beside the ring and the partial sums
-    const int per_chunk = 2048 * nt + 32 * nt + (p.off ? 128 * nt : 0);
+    const int per_unit = uc * (2048 * nt + 32 * nt + (p.off ? 128 * nt : 0));
 
     // The split of K over a cluster (C) and over a CTA's warps (KS), by an
-    // estimate in nanoseconds from sweeps on a B200: a warp's unit takes 370
-    // (NT = 2: 560) beside 15 others; a (chunk, token) of x 6 to stage; the
-    // join reads C KS sums an output, from other CTAs at 150 against 60 each
-    // round.  4096 x 4096, one token: C, KS = 1, 8 6.2 us, 4, 4 7.4, 1, 1
-    // 11.5; 4096 x 14336, 16 tokens: 4, 2 22.8, 1, 1 66.9; 65536 x 8192, 16
-    // tokens: 4, 1 115, 1, 8 287.
+    // estimate in nanoseconds from sweeps on a B200: a warp's 128-column chunk
+    // takes 480 (NT = 2: 800) beside 15 others; a (chunk, token) of x 12 to
+    // stage; the join reads C KS sums an output, from other CTAs at 150 against
+    // 60 each round, and a wave of partial sums more costs 1500.  4096 x 4096, one token: C, KS = 1, 8 5.6 us, 4, 4 6.9,
+    // 1, 1 9.5; 4096 x 14336 INT4, 4 tokens: 4, 2 17.5, 1, 8 25.4, 1, 1 56.7;
+    // 65536 x 8192, 16 tokens: 4, 1 107, 1, 1 131, 1, 8 285.
     GvKernel k = gv_pick(p.elem, mode, bc, nt);
     if (raise_smem_limit(reinterpret_cast<const void *>(k), kGvSmem)) return 1;
     const int toks = (int)(p.M < p.group ? p.M : p.group);
     int64_t best = -1;
     for (int C = 1; C <= 8; C *= 2) {
-        const int cpc = (p.chunks + C - 1) / C;
+        const int cpc = (p.units + C - 1) / C;
         const int64_t lim = resident_clusters(C);
         const int64_t ncl = tiles < lim ? tiles : lim;
         const int64_t per = (tiles + ncl - 1) / ncl;
-        const bool fits = (int64_t)cpc * per_chunk <= x_room;
+        const bool fits = (int64_t)cpc * per_unit <= x_room;
         for (int KS = 1; KS <= kGvWarps; KS *= 2) {
             const int64_t tg = kGvWarps / KS;
             const int64_t units = ((per + tg - 1) / tg) * ((cpc + KS - 1) / KS);
-            const int64_t waves = fits ? 1 : 1 + per * KS * kGvPart * 4 * nt / (32 * 1024);
+            const int64_t x_bytes = (fits ? cpc : x_room / per_unit) * (int64_t)per_unit;
+            const int64_t held = (kGvSmem - ring - x_bytes) / ((KS * kGvPart * nt + 16) * 4);
+            const int64_t waves = held < 1 ? 1000 : (per + held - 1) / held;
             const int64_t rounds = (per * 4 * toks + C * kGvThreads - 1) / (C * kGvThreads);
-            const int64_t cost = units * (nt == 1 ? 370 : 560) + waves * cpc * toks * 6 +
-                                 rounds * C * KS * (C > 1 ? 150 : 60) + (C > 1 ? 500 : 0);
+            const int64_t cost = units * uc * (nt == 1 ? 480 : 800) + (fits ? 1 : waves) * cpc * uc * toks * 12 +
+                                 rounds * C * KS * (C > 1 ? 150 : 60) + (C > 1 ? 500 : 0) + (waves - 1) * 1500;
             if (best < 0 || cost < best) {
                 best = cost;
                 gm.C = C;
@@ -113,13 +116,13 @@ int launch_gemv(GvParams p, cudaStream_t st)
             }
         }
     }
-    const int xc_max = x_room / per_chunk;
+    const int xc_max = x_room / per_unit;
     if (gm.xc > xc_max) gm.xc = xc_max;
     if (gm.xc < 1) gm.xc = 1;
     int at = ring;
-    gm.xs_at = at; at += gm.xc * 2048 * nt;
-    gm.ex_at = at; at += gm.xc * 32 * nt;
-    gm.xsum_at = at; at += p.off ? gm.xc * 128 * nt : 0;
+    gm.xs_at = at; at += gm.xc * uc * 2048 * nt;
+    gm.ex_at = at; at += gm.xc * uc * 32 * nt;
+    gm.xsum_at = at; at += p.off ? gm.xc * uc * 128 * nt : 0;
     gm.part_at = at;
     const int64_t ncl_max = resident_clusters(gm.C);
     const int64_t ncl = tiles < ncl_max ? tiles : ncl_max;

@@ -17,17 +17,18 @@
 //   2^-31 of its chunk's largest is one f16 exactly; a binary32 value is the
 //   sum of two (11 + 12 bits) exactly, the second scaled by 2^11.  Smaller
 //   values are rounded at 2^-39 (bf16) or 2^-50 of the chunk's largest.
-// * Work is split into units of 16 rows x 128 columns.  A cluster of C CTAs
+// * Work is split into units of 16 rows x 256 columns (128 where K is no
+//   multiple of 256).  A cluster of C CTAs
 //   splits K (each CTA keeps its slice of x in shared memory), its CTAs' 16
 //   warps split rows and, KS ways, the slice.  Each warp streams its units
 //   through a private ring of asynchronous 16-byte copies (no registers, no
 //   CTA barrier), and the partial sums of a row tile meet once, through
 //   distributed shared memory, in a fixed order: results do not depend on
 //   timing, and no workspace is needed.
-// * A warp's unit in shared memory: 16 rows x 64 bytes, 16-byte pieces
-//   XOR-swizzled by row pair, so that lane (g, t) reads word t of a block's
-//   16 bytes for rows g and g + 8 without bank conflicts: the four lanes of
-//   a row share a block, hence its scale, in each matrix instruction.
+// * A warp's unit in shared memory: 16 rows of 16-byte pieces, XOR-swizzled by
+//   row, so that lane (g, t) reads word t of a block's 16 bytes for rows g and
+//   g + 8 without bank conflicts: the four lanes of a row share a block, hence
+//   its scale, in each matrix instruction.
 #pragma once
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -43,27 +44,35 @@ namespace mxk {
 
 constexpr int kGvWarps = 16;
 constexpr int kGvThreads = kGvWarps * 32;
-constexpr int kGvStages = 4;
 constexpr int kGvPart = 8 * 20;   // floats of a tile's partial sums of 8 columns
 
-// How a unit's scales are laid out:
-//   GM_BLOCK  blocks of 8, 16 or 32 and K a multiple of 128: 128 / B scales of
-//             a row are whole words (row-major or chunked), no ragged chunk;
-//   GM_GROUP  blocks of 128 or 256: one scale (and offset) a row;
-//   GM_ANY    everything else: windows of aligned words around the scales,
-//             a ragged last chunk, macro scales, offsets of small blocks.
+// How a unit's scales are laid out, and how wide the unit is:
+//   GM_BLOCK  blocks of 8, 16 or 32 and K a multiple of 256: 256 columns, whose
+//             256 / B scales of a row are whole words (row-major or chunked);
+//   GM_GROUP  blocks of 128 or 256, K a multiple of 256: 256 columns, two
+//             scales (and offsets) of a row, or one;
+//   GM_ANY    everything else, 128 columns: windows of aligned words around
+//             the scales, a ragged last chunk, macro scales, offsets of small
+//             blocks.
+// The wide units' 128-byte rows halve the addresses, waits and scale reads of
+// a chunk (65536 x 8192, one token: 128-column units 64 us).
 enum { GM_BLOCK = 0, GM_GROUP = 1, GM_ANY = 2 };
+
+// 128-column chunks of a unit, ring stages
+__host__ __device__ constexpr int gv_chunks(int mode) { return mode == GM_ANY ? 1 : 2; }
+__host__ __device__ constexpr int gv_stages(int mode) { return mode == GM_ANY ? 4 : 3; }
 
 // scale words of a row in a stage.  GM_ANY: enough for the aligned words that
 // cover 128 / B scales anywhere (BC 32: up to 4 in 2 words; 16: 8 at an even
 // byte in 3; 8: 16 in 4)
 template <int MODE, int BC> __host__ __device__ constexpr int gv_scale_words()
 {
-    return MODE == GM_BLOCK ? 32 / BC : MODE == GM_GROUP ? 1 : BC == 32 ? 2 : 4;
+    return MODE == GM_BLOCK ? 64 / BC : MODE == GM_GROUP ? 1 : BC == 32 ? 2 : 4;
 }
 // one ring stage of a warp: codes, scales, offsets (GM_GROUP a word a row,
-// GM_ANY four), macro bytes
-template <int MODE, int BC> __host__ __device__ constexpr int gv_off_at() { return 1024 + 64 * gv_scale_words<MODE, BC>(); }
+// GM_ANY four), macro bytes; a multiple of the code row for GM_BLOCK, GM_GROUP
+template <int MODE> __host__ __device__ constexpr int gv_sc_at() { return 1024 * gv_chunks(MODE); }
+template <int MODE, int BC> __host__ __device__ constexpr int gv_off_at() { return gv_sc_at<MODE>() + 64 * gv_scale_words<MODE, BC>(); }
 template <int MODE, int BC> __host__ __device__ constexpr int gv_mac_at()
 {
     return gv_off_at<MODE, BC>() + (MODE == GM_GROUP ? 64 : MODE == GM_ANY && BC == 32 ? 256 : 0);
@@ -75,7 +84,7 @@ template <int MODE, int BC> __host__ __device__ constexpr int gv_stage_bytes()
 
 struct GvGeom {
     int xs_at, ex_at, xsum_at, part_at;  // shared-memory places
-    int xc;            // chunks of x held at a time
+    int xc;            // x held at a time, in units of columns
     int tiles_wave;    // row tiles whose partial sums are held
     int tile_floats;   // stride of a row tile's partial sums: 16 mod 32, so that a join's reads spread over the banks
     int C, KS;
@@ -84,8 +93,8 @@ struct GvGeom {
 // Where a lane's copies of a row tile come from (32-bit: a call has fewer than
 // 2^32 weights).
 struct GvSource {
-    uint32_t code[2];   // bytes: rows g and g + 8, 16-byte piece t of chunk 0
-    uint32_t sc[2];     // scales of the rows this lane copies words of
+    uint32_t code[2];   // bytes: rows g and g + 8, 16-byte piece t of unit 0
+    uint32_t sc[4];     // scales of the rows this lane copies words of
     uint32_t off[2];
     uint32_t mac;
 };
@@ -96,47 +105,61 @@ __device__ __forceinline__ void gv_source(const GvParams &p, GvSource &src, uint
     constexpr int W = gv_scale_words<MODE, BC>();
     const uint32_t row0 = tile * 16, last = (uint32_t)p.N - 1, S = (uint32_t)p.S;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t row = min(row0 + (lane >> 2) + 8 * i, last);
-        src.code[i] = row * (uint32_t)(p.K >> 1) + (lane & 3) * 16;
+    for (int i = 0; i < 4; ++i) {
+        if (i < 2) {
+            const uint32_t row = min(row0 + (lane >> 2) + 8 * i, last);
+            src.code[i] = row * (uint32_t)(p.K >> 1) + (lane & 3) * 16;
+            if (MODE == GM_ANY) src.off[i] = min(row0 + (lane + 32 * i) / 4, last) * S;
+        }
         if (32 * i < 16 * W) {
             const int w = (lane + 32 * i) % W;
             const uint32_t r = min(row0 + ((lane + 32 * i) / W & 15), last);
             const uint32_t base = p.sf_chunk ? (uint32_t)sf_chunk_index(r, 0, 0) + (r >> 7) * (S >> 2) * 512u : r * S;
             src.sc[i] = base + (MODE == GM_BLOCK ? w * (p.sf_chunk ? 512u : 4u) : 0u);
         }
-        if (MODE == GM_ANY) src.off[i] = min(row0 + (lane + 32 * i) / 4, last) * S;
     }
     if (MODE == GM_GROUP) src.off[0] = min(row0 + (lane & 15), last) * S;
     if (MODE == GM_ANY) src.mac = min(row0 + (lane & 15), last) * (uint32_t)(p.K >> 7);
 }
 
-// Copy a unit (the source's tile, chunk) into a stage.
+// Copy a unit (the source's tile, unit u of its columns) into a stage.
 template <int MODE, int BC>
-__device__ __forceinline__ void gv_issue(const GvParams &p, uint32_t stage, const GvSource &src, uint32_t chunk, int lane)
+__device__ __forceinline__ void gv_issue(const GvParams &p, uint32_t stage, const GvSource &src, uint32_t u, int lane)
 {
     constexpr int W = gv_scale_words<MODE, BC>();
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t left = (uint32_t)p.K - chunk * 128u;   // columns from this chunk on
-    const bool in = MODE != GM_ANY || t * 32u < left;
+    if (MODE != GM_ANY) {
+        // rows of eight pieces, piece b of row r at place b ^ (r & 7)
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-        cp_async16(stage + (g + 8 * i) * 64 + ((t ^ ((g >> 1) & 3)) << 4), p.codes + (in ? src.code[i] + chunk * 64u : 0u),
-                   in ? 16 : 0);
+        for (int i = 0; i < 2; ++i) {
+            const uint8_t *from = p.codes + (src.code[i] + u * 128u);
+            const uint32_t to = stage + (g + 8 * i) * 128 + ((t ^ g) << 4);
+            cp_async16(to, from, 16);
+            cp_async16(to ^ 64u, from + 64, 16);
+        }
+    } else {
+        const uint32_t left = (uint32_t)p.K - u * 128u;   // columns from this chunk on
+        const bool in = t * 32u < left;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            cp_async16(stage + (g + 8 * i) * 64 + ((t ^ ((g >> 1) & 3)) << 4), p.codes + (in ? src.code[i] + u * 64u : 0u),
+                       in ? 16 : 0);
+    }
+    const uint32_t sc = stage + gv_sc_at<MODE>();
     if (MODE == GM_BLOCK) {
         const uint32_t step = p.sf_chunk ? 512u * W : 4u * W;
-        if (W >= 2 || lane < 16) cp_async4(stage + 1024 + lane * 4, p.scales + (src.sc[0] + chunk * step), 4);
-        if (W == 4) cp_async4(stage + 1024 + 128 + lane * 4, p.scales + (src.sc[1] + chunk * step), 4);
+#pragma unroll
+        for (int i = 0; i < W / 2; ++i) cp_async4(sc + (lane + 32 * i) * 4, p.scales + (src.sc[i] + u * step), 4);
         return;
     }
-    const uint32_t j0 = (chunk * 128u) >> p.log2B, n_scales = (uint32_t)p.n_scales;
-    // the aligned words covering the chunk's scales of every row
+    const uint32_t j0 = (u * (128u * gv_chunks(MODE))) >> p.log2B, n_scales = (uint32_t)p.n_scales;
+    // the aligned words covering the unit's scales of every row
 #pragma unroll
     for (int i = 0; i < (W + 1) / 2; ++i) {
         const int w = (lane + 32 * i) % W;
         const uint32_t at = p.sf_chunk ? src.sc[i] + ((j0 >> 2) + w) * 512u : ((src.sc[i] + j0) & ~3u) + 4 * w;
         const int nb = at + 4 <= n_scales ? 4 : at < n_scales ? (int)(n_scales - at) : 0;
-        if (W >= 2 || lane < 16) cp_async4(stage + 1024 + (lane + 32 * i) * 4, p.scales + (nb ? at : 0u), nb);
+        if (W >= 2 || lane < 16) cp_async4(sc + (lane + 32 * i) * 4, p.scales + (nb ? at : 0u), nb);
     }
     if (p.off && (MODE == GM_GROUP || BC == 32)) {
         // bf16 offsets, row-major whatever the scales' layout: the aligned
@@ -152,30 +175,20 @@ __device__ __forceinline__ void gv_issue(const GvParams &p, uint32_t stage, cons
         }
     }
     if (MODE == GM_ANY && p.macro && lane < 16) {
-        const uint32_t at = (src.mac + chunk) & ~3u, n = (uint32_t)p.N * (uint32_t)(p.K >> 7);
+        const uint32_t at = (src.mac + u) & ~3u, n = (uint32_t)p.N * (uint32_t)(p.K >> 7);
         cp_async4(stage + gv_mac_at<MODE, BC>() + lane * 4, p.macro + at, at + 4 <= n ? 4 : (int)(n - at));
     }
 }
 
-// Scales of one row's blocks in a unit, macro scale included.  at: the row's
-// first scale (row S); mat: its first macro scale.
-template <int MODE, int BC>
+// Scales of one row's blocks in a 128-column unit, macro scale included.  at:
+// the row's first scale (row S); mat: its first macro scale.
+template <int BC>
 __device__ __forceinline__ void gv_scales(const GvParams &p, uint32_t stage, uint32_t at, uint32_t mat, int r,
                                           uint32_t chunk, float *s)
 {
-    constexpr int W = gv_scale_words<MODE, BC>();
-    const uint32_t sc = stage + 1024 + r * W * 4;
-    if (MODE == GM_BLOCK) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) scales4(p.sfmt, lds32(sc + 4 * i), s + 4 * i);
-        return;
-    }
+    const uint32_t sc = stage + 1024 + r * gv_scale_words<GM_ANY, BC>() * 4;
     const uint32_t j0 = (chunk * 128u) >> p.log2B;
     const int sh = (int)((p.sf_chunk ? j0 : at + j0) & 3u) * 8;
-    if (MODE == GM_GROUP) {
-        s[0] = scale1(p.sfmt, (lds32(sc) >> sh) & 0xffu);
-        return;
-    }
     if (BC == 32) {
         uint32_t w = __funnelshift_r(lds32(sc), lds32(sc + 4), sh);
         if (p.log2B == 6) w = __byte_perm(w, 0u, 0x1100u);
@@ -198,7 +211,7 @@ __device__ __forceinline__ void gv_scales(const GvParams &p, uint32_t stage, uin
             if (i * BC >= left) s[i] = 0.0f;
     }
     if (p.macro) {
-        const uint32_t w = lds32(stage + gv_mac_at<MODE, BC>() + r * 4);
+        const uint32_t w = lds32(stage + gv_mac_at<GM_ANY, BC>() + r * 4);
         const float m = e4m3_value((w >> (8 * ((mat + chunk) & 3u))) & 0xffu);
 #pragma unroll
         for (int i = 0; i < 128 / BC; ++i) s[i] = __fmul_rn(s[i], m);
@@ -353,109 +366,138 @@ __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, i
 // INT4 words whose eight codes share a block are decoded in pairs (i, i + 4)
 template <int ELEM, int BC> __host__ __device__ constexpr bool gv_spread() { return BC == 32 && (ELEM == GE_INT4 || ELEM == GE_UINT4); }
 
-// One unit of a warp: acc += (16 rows x 128 columns of codes in the stage) x
-// (chunk cx of the staged x).
+// A lane's codes of 32-block b of a row (its 16-byte piece at `at`, the lane's
+// word of it included) -> four f16x2.  OFF: bytes to the row.
+template <int ELEM, int BC, int OFF>
+__device__ __forceinline__ void gv_codes(uint32_t at, int t, uint32_t h[4])
+{
+    uint32_t w;
+    if (BC == 32) {
+        w = lds32(at + OFF);
+    } else if (BC == 16) {
+        // 16-bit pieces t and t + 4: four codes of each 16-block
+        w = __byte_perm(lds32(at + OFF), lds32(at + OFF + 8), (t & 1) ? 0x7632u : 0x5410u);
+    } else {
+        // byte t of each 8-block
+        const uint4 x = lds128(at + OFF);
+        const uint32_t sel = (uint32_t)t | ((uint32_t)(t + 4) << 4);
+        w = __byte_perm(__byte_perm(x.x, x.y, sel), __byte_perm(x.z, x.w, sel), 0x5410u);
+    }
+    if constexpr (gv_spread<ELEM, BC>()) int4_halves_spread<ELEM>(w, h);
+    else codes8_halves<ELEM>(w, h);
+}
+
+// One unit of a warp: acc += (16 rows x the unit's columns of codes in the
+// stage) x (its chunks of the staged x).
 template <int ELEM, int MODE, int BC, int NT>
 __device__ __forceinline__ void gv_unit(const GvParams &p, uint32_t st, uint32_t xs, const float *ex, const float *xsum,
-                                        uint32_t a_lo, uint32_t a_hi, uint32_t m_lo, uint32_t m_hi, uint32_t chunk,
+                                        uint32_t a_lo, uint32_t a_hi, uint32_t m_lo, uint32_t m_hi, uint32_t unit,
                                         int lane, float acc[NT][4])
 {
     const int g = lane >> 2, t = lane & 3;
-    constexpr int NS = MODE == GM_GROUP ? 1 : 128 / BC;
-    float s_lo[NS], s_hi[NS];
-    gv_scales<MODE, BC>(p, st, a_lo, m_lo, g, chunk, s_lo);
-    gv_scales<MODE, BC>(p, st, a_hi, m_hi, g + 8, chunk, s_hi);
-    float ca[NT][4];
+    constexpr int UC = gv_chunks(MODE), NS = MODE == GM_GROUP ? 1 : 128 / BC, ROW = 64 * UC;
+    // the lane's word of piece 0 of row g, swizzle included; piece b of a row
+    // by exclusive or
+    const uint32_t place = MODE == GM_ANY ? 0u : st + g * ROW + (g << 4) + (BC == 32 ? 4 * t : BC == 16 ? 4 * (t >> 1) : 0);
+    uint32_t gs_lo = 0u, gs_hi = 0u;
+    if (MODE == GM_GROUP) {
+        // the unit's scales of a row: one or two bytes of the word
+        const uint32_t j0 = (unit * 256u) >> p.log2B;
+        gs_lo = lds32(st + gv_sc_at<MODE>() + g * 4) >> (8 * ((p.sf_chunk ? j0 : a_lo + j0) & 3u));
+        gs_hi = lds32(st + gv_sc_at<MODE>() + (g + 8) * 4) >> (8 * ((p.sf_chunk ? j0 : a_hi + j0) & 3u));
+    }
 #pragma unroll
-    for (int b = 0; b < 4; ++b) {
-        const uint32_t pl = st + g * 64 + ((b ^ ((g >> 1) & 3)) << 4);
-        const uint32_t ph = pl + 512;
-        uint32_t wl, wh;
-        if (BC == 32) {
-            wl = lds32(pl + 4 * t);
-            wh = lds32(ph + 4 * t);
-        } else if (BC == 16) {
-            // 16-bit pieces t and t + 4: four codes of each 16-block
-            const uint32_t sel = (t & 1) ? 0x7632u : 0x5410u;
-            wl = __byte_perm(lds32(pl + 4 * (t >> 1)), lds32(pl + 8 + 4 * (t >> 1)), sel);
-            wh = __byte_perm(lds32(ph + 4 * (t >> 1)), lds32(ph + 8 + 4 * (t >> 1)), sel);
+    for (int c = 0; c < UC; ++c) {
+        float s_lo[NS], s_hi[NS];
+        if (MODE == GM_BLOCK) {
+            constexpr int W = 32 / BC;   // words of a chunk
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                scales4(p.sfmt, lds32(st + gv_sc_at<MODE>() + (g * UC * W + c * W + i) * 4), s_lo + 4 * i);
+                scales4(p.sfmt, lds32(st + gv_sc_at<MODE>() + ((g + 8) * UC * W + c * W + i) * 4), s_hi + 4 * i);
+            }
+        } else if (MODE == GM_GROUP) {
+            const int sh = c && p.log2B == 7 ? 8 : 0;
+            s_lo[0] = scale1(p.sfmt, (gs_lo >> sh) & 0xffu);
+            s_hi[0] = scale1(p.sfmt, (gs_hi >> sh) & 0xffu);
         } else {
-            // byte t of each 8-block
-            const uint4 x0 = lds128(pl), x1 = lds128(ph);
-            const uint32_t sel = (uint32_t)t | ((uint32_t)(t + 4) << 4);
-            wl = __byte_perm(__byte_perm(x0.x, x0.y, sel), __byte_perm(x0.z, x0.w, sel), 0x5410u);
-            wh = __byte_perm(__byte_perm(x1.x, x1.y, sel), __byte_perm(x1.z, x1.w, sel), 0x5410u);
+            gv_scales<BC>(p, st, a_lo, m_lo, g, unit, s_lo);
+            gv_scales<BC>(p, st, a_hi, m_hi, g + 8, unit, s_hi);
         }
-        uint32_t hl[4], hh[4];
-        if constexpr (gv_spread<ELEM, BC>()) {
-            int4_halves_spread<ELEM>(wl, hl);
-            int4_halves_spread<ELEM>(wh, hh);
-        } else {
-            codes8_halves<ELEM>(wl, hl);
-            codes8_halves<ELEM>(wh, hh);
+        float ca[NT][4];
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            // (a 128-column stage is no multiple of its rows: the piece's place
+            // by itself)
+            const uint32_t at = MODE == GM_ANY ? st + g * ROW + ((b ^ ((g >> 1) & 3)) << 4) + (BC == 32 ? 4 * t : BC == 16 ? 4 * (t >> 1) : 0)
+                                               : place ^ ((4 * c + b) << 4);
+            uint32_t hl[4], hh[4];
+            gv_codes<ELEM, BC, 0>(at, t, hl);
+            gv_codes<ELEM, BC, 8 * ROW>(at, t, hh);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const uint4 xb = lds128(xs + (((4 * c + b) * NT + n) << 9) + lane * 16);
+                if (MODE == GM_GROUP) {
+                    // one scale for the whole chunk: one sum
+                    if (b == 0) mma_16816_zero(ca[n], hl[0], hh[0], hl[1], hh[1], xb.x, xb.y);
+                    else mma_16816(ca[n], hl[0], hh[0], hl[1], hh[1], xb.x, xb.y);
+                    mma_16816(ca[n], hl[2], hh[2], hl[3], hh[3], xb.z, xb.w);
+                    continue;
+                }
+                const uint32_t xw[4] = {xb.x, xb.y, xb.z, xb.w};
+                constexpr int PER = 32 / BC == 0 ? 1 : 32 / BC;   // scales of a 32-block
+#pragma unroll
+                for (int i = 0; i < PER; ++i) {
+                    float d[4];
+                    if (BC == 32) {
+                        mma_16816_zero(d, hl[0], hh[0], hl[1], hh[1], xw[0], xw[1]);
+                        mma_16816(d, hl[2], hh[2], hl[3], hh[3], xw[2], xw[3]);
+                    } else if (BC == 16) {
+                        mma_16816_zero(d, hl[2 * i & 3], hh[2 * i & 3], hl[(2 * i + 1) & 3], hh[(2 * i + 1) & 3], xw[2 * i & 3],
+                                       xw[(2 * i + 1) & 3]);
+                    } else {
+                        mma_1688_zero(d, hl[i], hh[i], xw[i]);
+                    }
+                    const float sl = s_lo[(b * PER + i) % NS], sh = s_hi[(b * PER + i) % NS];
+                    if (b == 0 && i == 0) {
+                        ca[n][0] = __fmul_rn(sl, d[0]);
+                        ca[n][1] = __fmul_rn(sl, d[1]);
+                        ca[n][2] = __fmul_rn(sh, d[2]);
+                        ca[n][3] = __fmul_rn(sh, d[3]);
+                    } else {
+                        ca[n][0] = fmaf(sl, d[0], ca[n][0]);
+                        ca[n][1] = fmaf(sl, d[1], ca[n][1]);
+                        ca[n][2] = fmaf(sh, d[2], ca[n][2]);
+                        ca[n][3] = fmaf(sh, d[3], ca[n][3]);
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            const uint4 xb = lds128(xs + ((b * NT + n) << 9) + lane * 16);
+            float2 e = *reinterpret_cast<const float2 *>(ex + (c * NT + n) * 8 + 2 * t);
+            float2 f = e;
             if (MODE == GM_GROUP) {
-                // one scale for the whole chunk: one sum
-                if (b == 0) mma_16816_zero(ca[n], hl[0], hh[0], hl[1], hh[1], xb.x, xb.y);
-                else mma_16816(ca[n], hl[0], hh[0], hl[1], hh[1], xb.x, xb.y);
-                mma_16816(ca[n], hl[2], hh[2], hl[3], hh[3], xb.z, xb.w);
-                continue;
+                // the scale with the power of two: exact while in range
+                f = make_float2(__fmul_rn(e.x, s_hi[0]), __fmul_rn(e.y, s_hi[0]));
+                e = make_float2(__fmul_rn(e.x, s_lo[0]), __fmul_rn(e.y, s_lo[0]));
             }
-            const uint32_t xw[4] = {xb.x, xb.y, xb.z, xb.w};
-            constexpr int PER = 32 / BC == 0 ? 1 : 32 / BC;   // scales of a 32-block
-#pragma unroll
-            for (int i = 0; i < PER; ++i) {
-                float d[4];
-                if (BC == 32) {
-                    mma_16816_zero(d, hl[0], hh[0], hl[1], hh[1], xw[0], xw[1]);
-                    mma_16816(d, hl[2], hh[2], hl[3], hh[3], xw[2], xw[3]);
-                } else if (BC == 16) {
-                    mma_16816_zero(d, hl[2 * i & 3], hh[2 * i & 3], hl[(2 * i + 1) & 3], hh[(2 * i + 1) & 3], xw[2 * i & 3],
-                                   xw[(2 * i + 1) & 3]);
-                } else {
-                    mma_1688_zero(d, hl[i], hh[i], xw[i]);
-                }
-                const float sl = s_lo[(b * PER + i) % NS], sh = s_hi[(b * PER + i) % NS];
-                if (b == 0 && i == 0) {
-                    ca[n][0] = __fmul_rn(sl, d[0]);
-                    ca[n][1] = __fmul_rn(sl, d[1]);
-                    ca[n][2] = __fmul_rn(sh, d[2]);
-                    ca[n][3] = __fmul_rn(sh, d[3]);
-                } else {
-                    ca[n][0] = fmaf(sl, d[0], ca[n][0]);
-                    ca[n][1] = fmaf(sl, d[1], ca[n][1]);
-                    ca[n][2] = fmaf(sh, d[2], ca[n][2]);
-                    ca[n][3] = fmaf(sh, d[3], ca[n][3]);
-                }
-            }
+            acc[n][0] = fmaf(e.x, ca[n][0], acc[n][0]);
+            acc[n][1] = fmaf(e.y, ca[n][1], acc[n][1]);
+            acc[n][2] = fmaf(f.x, ca[n][2], acc[n][2]);
+            acc[n][3] = fmaf(f.y, ca[n][3], acc[n][3]);
         }
-    }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        float2 e = *reinterpret_cast<const float2 *>(ex + n * 8 + 2 * t);
-        float2 f = e;
-        if (MODE == GM_GROUP) {
-            // the scale with the power of two: exact while in range
-            f = make_float2(__fmul_rn(e.x, s_hi[0]), __fmul_rn(e.y, s_hi[0]));
-            e = make_float2(__fmul_rn(e.x, s_lo[0]), __fmul_rn(e.y, s_lo[0]));
-        }
-        acc[n][0] = fmaf(e.x, ca[n][0], acc[n][0]);
-        acc[n][1] = fmaf(e.y, ca[n][1], acc[n][1]);
-        acc[n][2] = fmaf(f.x, ca[n][2], acc[n][2]);
-        acc[n][3] = fmaf(f.y, ca[n][3], acc[n][3]);
     }
     if (!p.off || MODE == GM_BLOCK || (MODE == GM_ANY && BC != 32)) return;
-    // block offsets times the sums of x over the blocks
-    const uint32_t j0 = (chunk * 128u) >> p.log2B;
+    // block offsets times the sums of x over the blocks (GM_GROUP: over the
+    // chunks; a block of 256 has one offset for both)
     const uint32_t ob = st + gv_off_at<MODE, BC>(), row = MODE == GM_GROUP ? 4u : 16u;
+    const uint32_t j0 = (unit * (128u * UC)) >> p.log2B;
     const uint32_t ol = ob + g * row + 2 * ((a_lo + j0) & 1u), oh = ob + (g + 8) * row + 2 * ((a_hi + j0) & 1u);
 #pragma unroll
-    for (int b = 0; b < (MODE == GM_GROUP ? 1 : 4); ++b) {
-        if (MODE == GM_ANY && chunk * 128u + b * 32u >= (uint32_t)p.K) break;
-        const uint32_t j = MODE == GM_GROUP ? 0u : ((b * 32u) >> p.log2B) * 2u;
+    for (int b = 0; b < (MODE == GM_GROUP ? UC : 4); ++b) {
+        if (MODE == GM_ANY && unit * 128u + b * 32u >= (uint32_t)p.K) break;
+        const uint32_t j = ((MODE == GM_GROUP ? b * 128u : b * 32u) >> p.log2B) * 2u;
         const float fl = bits2f(lds16(ol + j) << 16), fh = bits2f(lds16(oh + j) << 16);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -474,7 +516,7 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
 {
     extern __shared__ __align__(128) uint8_t smem[];
     cg::cluster_group cluster = cg::this_cluster();
-    constexpr int SB = gv_stage_bytes<MODE, BC>();
+    constexpr int SB = gv_stage_bytes<MODE, BC>(), UC = gv_chunks(MODE), STAGES = gv_stages(MODE);
     constexpr bool SPREAD = gv_spread<ELEM, BC>();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -485,10 +527,10 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
     const int P = p.x_fp32 ? 2 : 1;
     const uint32_t tiles = (uint32_t)((p.N + 15) >> 4);
     const int mine = cl < tiles ? (int)((tiles - cl + ncl - 1) / ncl) : 0;   // tiles cl, cl + ncl, ...
-    const int c_lo = (int)((int64_t)p.chunks * rank / gm.C), c_hi = (int)((int64_t)p.chunks * (rank + 1) / gm.C);
+    const int c_lo = (int)((int64_t)p.units * rank / gm.C), c_hi = (int)((int64_t)p.units * (rank + 1) / gm.C);
     const int ks = warp % gm.KS, tg = warp / gm.KS, TG = kGvWarps / gm.KS;
     const uint32_t sbase = (uint32_t)__cvta_generic_to_shared(smem);
-    const uint32_t ring = sbase + warp * kGvStages * SB, ring_end = ring + kGvStages * SB;
+    const uint32_t ring = sbase + warp * STAGES * SB, ring_end = ring + STAGES * SB;
     float *part = reinterpret_cast<float *>(smem + gm.part_at);
     const float *ex = reinterpret_cast<const float *>(smem + gm.ex_at);
     const float *xsum = reinterpret_cast<const float *>(smem + gm.xsum_at);
@@ -519,11 +561,11 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
                 cp_async_commit();
             };
 #pragma unroll
-            for (int i = 0; i < kGvStages - 1; ++i) issue();
+            for (int i = 0; i < STAGES - 1; ++i) issue();
             if (!resident || w0 == 0) {
                 if (s0 != c_lo || w0 != 0) __syncthreads();   // the last slice of x is no longer read
-                if (p.x_fp32) gv_stage_x<BC, NT, true, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0, sn);
-                else gv_stage_x<BC, NT, false, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0, sn);
+                if (p.x_fp32) gv_stage_x<BC, NT, true, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0 * UC, sn * UC);
+                else gv_stage_x<BC, NT, false, SPREAD, MODE == GM_GROUP>(p, gm, smem, tok0, toks, s0 * UC, sn * UC);
                 __syncthreads();
             }
             uint32_t st = ring;
@@ -539,11 +581,11 @@ __global__ void __launch_bounds__(kGvThreads, 1) k_gemv(const __grid_constant__ 
                     for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
                 int cx = a - s0;
                 for (int c = 0; c < nc; ++c, ++cx) {
-                    cp_async_wait<kGvStages - 2>();
+                    cp_async_wait<STAGES - 2>();
                     __syncwarp();   // every lane's copies of this unit are in, and the last unit is read
                     issue();
-                    gv_unit<ELEM, MODE, BC, NT>(p, st, sbase + gm.xs_at + cx * (NT << 11), ex + cx * NT * 8,
-                                                xsum + cx * NT * (MODE == GM_GROUP ? 8 : 32), a_lo, a_hi, m_lo, m_hi, a + c, lane, acc);
+                    gv_unit<ELEM, MODE, BC, NT>(p, st, sbase + gm.xs_at + cx * UC * (NT << 11), ex + cx * UC * NT * 8,
+                                                xsum + cx * UC * NT * (MODE == GM_GROUP ? 8 : 32), a_lo, a_hi, m_lo, m_hi, a + c, lane, acc);
                     st = st + SB == ring_end ? ring : st + SB;
                 }
                 // this warp's partial sums of the tile: 16 rows of each

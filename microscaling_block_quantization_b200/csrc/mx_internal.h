@@ -95,7 +95,7 @@ struct GvParams {
     void *y;
     int64_t ldy;
     int y_fp32;
-    int group, chunks;       // tokens of a launch row, 128-column chunks (set by launch_gemv)
+    int group, units;        // tokens of a launch row, units of a row's columns (set by launch_gemv)
 };
 
 // mx_kv_append: tokens' queries, keys and values, cache rows out
