@@ -9,12 +9,14 @@ Low-level functions carry the C names (``mx_quantize``, ``mx_dequantize``,
 ``mx_hadamard_quantize``, ``mx_qsnr``, ``mx_gemm``, ``mx_gemm_qsnr``, ...)
 and take raw device pointers; the high-level helpers (``quantize``,
 ``dequantize``, ``qsnr``, ``gemm``, ``gemm_qsnr``) allocate the outputs with
-torch and call them.
+torch and call them.  The decode-time operators (``gemv``, ``kv_append``,
+``attn_decode``) marshal in a compiled module (``csrc/binding.cpp``).
 """
 from __future__ import annotations
 
 import ctypes as C
 import dataclasses
+import importlib.util
 import os
 
 import torch
@@ -23,6 +25,7 @@ from . import inputs  # noqa: F401  (seeded synthetic workloads)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmx_b200.so")
+BINDING_PATH = os.path.join(_HERE, "_lib", "mx_binding.so")
 
 # ---- constants of include/mx.h ------------------------------------------
 MX_OK = 0
@@ -92,9 +95,19 @@ class Config:
         """The C struct by reference, built once per instance."""
         r = self.__dict__.get("_ref")
         if r is None:
-            r = C.byref(self.c())
+            c = self.c()
+            r = C.byref(c)
             object.__setattr__(self, "_ref", r)
+            object.__setattr__(self, "_address", C.addressof(c))    # (_ref keeps the struct)
         return r
+
+    def address(self) -> int:
+        """Where the C struct is, for the compiled binding."""
+        a = self.__dict__.get("_address")
+        if a is None:
+            self.ref()
+            a = self._address
+        return a
 
 
 MXFP4 = Config()
@@ -156,6 +169,24 @@ def lib() -> C.CDLL:
             getattr(L, f).restype = C.c_int
         _lib = L
     return _lib
+
+
+_compiled = None
+
+
+def _binding():
+    """The compiled marshalling of the decode-time operators."""
+    global _compiled
+    if _compiled is None:
+        lib()
+        if not os.path.exists(BINDING_PATH):
+            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+                               "`python -c 'import __graft_entry__ as g; g.build()'`")
+        spec = importlib.util.spec_from_file_location("mx_binding", BINDING_PATH)
+        m = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(m)
+        _compiled = m
+    return _compiled
 
 
 def mx_strerror(code: int) -> str:
@@ -514,59 +545,6 @@ def gemm(qa: Quantized, qb: Quantized, out_dtype: torch.dtype = torch.bfloat16,
 
 
 # ---- decode-time operators --------------------------------------------------
-_DT = {torch.bfloat16: DT_BF16, torch.float32: DT_FP32}
-
-
-class _Launch:
-    """Device and stream of a call that is not simply on the current ones: the
-    operands' device made current, and the caller's ``stream`` both for the
-    launch and for what the call allocates."""
-
-    __slots__ = ("ctx",)
-
-    def __init__(self, device, stream):
-        self.ctx = [torch.cuda.device(device)]
-        if stream is not None:
-            self.ctx.append(torch.cuda.stream(stream))
-
-    def __enter__(self):
-        for c in self.ctx:
-            c.__enter__()
-
-    def __exit__(self, *e):
-        for c in reversed(self.ctx):
-            c.__exit__(*e)
-
-
-def _elsewhere(device, stream) -> bool:
-    return stream is not None or device.index != torch.cuda.current_device()
-
-
-def _raw_stream(device) -> int:
-    return torch._C._cuda_getCurrentRawStream(device.index)
-
-
-def _same_device(device, *named) -> None:
-    """``named``: name, tensor or None, name, ..."""
-    for i in range(1, len(named), 2):
-        t = named[i]
-        if t is not None and t.device != device:
-            raise ValueError(f"{named[i - 1]} is on {t.device}, expected {device}")
-
-
-def _rows_of(t: torch.Tensor, name: str) -> int:
-    """Row stride of a 2-D tensor whose rows are contiguous."""
-    if t.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {t.dtype} of {name} (bf16 or fp32)")
-    if t.shape[1] > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    if t.shape[0] > 1:
-        if t.stride(0) < t.shape[1]:
-            raise ValueError(f"the rows of {name} overlap")
-        return t.stride(0)
-    return t.shape[1]
-
-
 def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *,
          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = x W^T of a few rows x (``[M, K]`` or ``[K]``, bf16 or fp32, rows at
@@ -575,36 +553,15 @@ def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *
     ``out_dtype`` or ``out`` (``[M, N]``, rows at any stride) says otherwise.
     On a ``stream`` of the caller's the result is allocated there; x and qw must
     be ready on it."""
-    if not x.is_cuda:
-        raise ValueError("x must be a CUDA tensor")
-    dev = x.device
-    if _elsewhere(dev, stream):
-        with _Launch(dev, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return gemv(x, qw, out_dtype, out=out)
-    N, K, shape = qw.rows, qw.cols, x.shape
-    if len(shape) not in (1, 2) or shape[-1] != K:
-        raise ValueError(f"x must be [M, {K}] or [{K}], got {list(shape)}")
-    x2 = x if len(shape) == 2 else x[None]
-    M = x2.shape[0]
-    ldx = _rows_of(x2, "x")
-    ts = qw.tensor_scale
-    _same_device(dev, "codes", qw.codes, "scales", qw.scales, "macro", qw.macro, "offsets", qw.offsets, "out", out,
-                 "tensor_scale", ts if qw.cfg.tensor_scale else None)
-    if out is None:
-        y = x.new_empty((M, N), dtype=out_dtype)
-        if y.dtype not in _DT:
-            raise TypeError(f"unsupported dtype {y.dtype} (bf16 or fp32)")
-        ldy = N
-    else:
-        if out.shape != shape[:-1] + (N,) or out.dtype != (out_dtype or out.dtype):
-            raise ValueError(f"out must be {list(shape[:-1]) + [N]} of {out_dtype or out.dtype}")
-        y = out if out.dim() == 2 else out[None]
-        ldy = _rows_of(y, "out")
-    rc = lib().mx_gemv(qw.cfg.ref(), x2.data_ptr(), _DT[x.dtype], ldx, M, qw.codes.data_ptr(), qw.scales.data_ptr(),
-                       _p(ts), _p(qw.macro), _p(qw.offsets), N, K, y.data_ptr(), _DT[y.dtype], ldy, _raw_stream(dev))
-    if rc:
-        _check("mx_gemv", rc)
-    return out if out is not None else y if len(shape) == 2 else y[0]
+    cfg = qw.cfg
+    r = _binding().gemv(x, qw.codes, qw.scales, qw.tensor_scale, qw.macro, qw.offsets, cfg.address(), cfg.tensor_scale, qw.rows,
+                        qw.cols, out_dtype, out)
+    if r.__class__ is int:
+        _check("mx_gemv", r)
+    return out if out is not None else r
 
 
 @dataclasses.dataclass
@@ -627,19 +584,27 @@ class KVCache:
         if r is None:
             rows, cols, bits = self.pages * self.page_size, self.kv_heads * self.head_dim, 8 if self.cfg.elem in FP6 else 4
             for name, t in (("k", self.k), ("v", self.v)):
-                _same_device(self.device, name + ".scales", t.scales, name + ".codes", t.codes,
-                             name + ".tensor_scale", t.tensor_scale if self.cfg.tensor_scale else None)
+                if any(u is not None and u.device != self.device for u in (t.codes, t.scales, t.tensor_scale if self.cfg.tensor_scale else None)):
+                    raise ValueError(f"{name}: every buffer must be on {self.device}")
                 if (t.codes.numel() * t.codes.element_size() < rows * cols * bits // 8 or not t.codes.is_contiguous() or
                         t.scales.numel() < rows * (cols // self.cfg.block) or not t.scales.is_contiguous()):
                     raise ValueError(f"{name}: buffers too small for {rows} rows of {cols}, or not contiguous")
                 if self.cfg.tensor_scale and (t.tensor_scale is None or t.tensor_scale.dtype != torch.float32):
                     raise TypeError(f"{name}: a float32 tensor scale is needed")
             ts = [t.tensor_scale.data_ptr() if self.cfg.tensor_scale else None for t in (self.k, self.v)]
-            r = C.byref(mx_kv_cache(self.k.codes.data_ptr(), self.v.codes.data_ptr(), self.k.scales.data_ptr(),
-                                    self.v.scales.data_ptr(), ts[0], ts[1], self.pages, self.page_size, self.kv_heads,
-                                    self.head_dim))
-            self.__dict__["_ref"] = r
+            c = mx_kv_cache(self.k.codes.data_ptr(), self.v.codes.data_ptr(), self.k.scales.data_ptr(),
+                            self.v.scales.data_ptr(), ts[0], ts[1], self.pages, self.page_size, self.kv_heads, self.head_dim)
+            r = C.byref(c)
+            self.__dict__["_ref"], self.__dict__["_address"] = r, C.addressof(c)
         return r
+
+    def address(self) -> int:
+        """Where the C struct is, for the compiled binding."""
+        a = self.__dict__.get("_address")
+        if a is None:
+            self.ref()
+            a = self._address
+        return a
 
     @property
     def device(self):
@@ -665,31 +630,6 @@ def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, cfg: Conf
     return KVCache(cfg, pages, page_size, kv_heads, head_dim, half(k_tensor_scale), half(v_tensor_scale))
 
 
-def _heads(t: torch.Tensor, heads: int, dim: int, name: str) -> int:
-    """Token stride of ``[T, heads * dim]`` or ``[T, heads, dim]`` with contiguous heads."""
-    shape, stride = t.shape, t.stride()
-    if len(shape) == 3 and shape[1] == heads and shape[2] == dim:
-        if stride[2] != 1 or (heads > 1 and stride[1] != dim):
-            raise ValueError(f"the heads of {name} must be contiguous")
-    elif not (len(shape) == 2 and shape[1] == heads * dim and (stride[1] == 1 or heads * dim == 0)):
-        raise ValueError(f"{name} must be [T, {heads * dim}] or [T, {heads}, {dim}] with contiguous heads, got "
-                         f"{list(shape)} with strides {stride}")
-    if shape[0] <= 1:
-        return heads * dim
-    if stride[0] < heads * dim:
-        raise ValueError(f"the tokens of {name} overlap")
-    return stride[0]
-
-
-def _vector(t, n, dtype, device, name):
-    """Pointer of an optional contiguous vector."""
-    if t is None:
-        return None
-    if t.dtype != dtype or t.device != device or t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be {n} contiguous {dtype} on {device}")
-    return t.data_ptr()
-
-
 def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
               positions: torch.Tensor | None = None, *, q_gain: torch.Tensor | None = None,
               k_gain: torch.Tensor | None = None, eps: float = 1e-6, inv_freq: torch.Tensor | None = None,
@@ -702,47 +642,15 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
     fused projection).  Returns ``(q_out, k_out)``: the rotated queries
     ``[T, q_heads, head_dim]`` (into ``q_out`` when given; it may be q) and, when ``k_out`` is
     True or a tensor, the rotated keys, else None."""
-    if not k.is_cuda:
-        raise ValueError("k must be a CUDA tensor")
-    dev, dt = k.device, k.dtype
-    if _elsewhere(dev, stream):
-        with _Launch(dev, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return kv_append(cache, q, k, v, slots, positions, q_gain=q_gain, k_gain=k_gain, eps=eps, inv_freq=inv_freq,
                              interleaved=interleaved, q_out=q_out, k_out=k_out)
-    D, H, T = cache.head_dim, cache.kv_heads, k.shape[0]
-    if dt not in _DT:
-        raise TypeError(f"unsupported dtype {dt} (bf16 or fp32)")
-    into = k_out if isinstance(k_out, torch.Tensor) else None
-    _same_device(dev, "the cache", cache.k.codes, "v", v, "q", q, "q_out", q_out, "k_out", into)
-    ldk, ldv = _heads(k, H, D, "k"), _heads(v, H, D, "v")
-    Hq = 0 if q is None else q.shape[1] if q.dim() == 3 else q.shape[1] // D
-    ldq = 0 if q is None else _heads(q, Hq, D, "q")
-    for name, t in (("v", v), ("q", q), ("q_out", q_out), ("k_out", into)):
-        if t is not None and (t.dtype != dt or t.shape[0] != T):
-            raise ValueError(f"{name} must have {T} tokens of {dt}")
-    rot = 0 if inv_freq is None else 2 * inv_freq.numel()
-    if rot and positions is None:
-        raise ValueError("a rotation needs positions")
-    ps = _vector(positions, T, torch.int64, dev, "positions")
-    pf = _vector(inv_freq, rot // 2, torch.float32, dev, "inv_freq")
-    pq, pk = _vector(q_gain, D, torch.float32, dev, "q_gain"), _vector(k_gain, D, torch.float32, dev, "k_gain")
-    pl = _vector(slots, T, torch.int64, dev, "slots")
-    ldqo, ldko = Hq * D, H * D
-    if q is None:
-        q_out = None
-    elif q_out is None:
-        q_out = k.new_empty((T, Hq, D))
-    else:
-        ldqo = _heads(q_out, Hq, D, "q_out")
-    if into is not None:
-        ldko = _heads(into, H, D, "k_out")
-    elif k_out is True:
-        into = k.new_empty((T, H, D))
-    rc = lib().mx_kv_append(cache.cfg.ref(), cache.ref(), _p(q), k.data_ptr(), v.data_ptr(), _DT[dt], ldq, ldk, ldv, T, Hq, pq, pk,
-                            eps, pf, rot, int(interleaved), ps, pl, _p(q_out), ldqo, _p(into), ldko, _raw_stream(dev))
-    if rc:
-        _check("mx_kv_append", rc)
-    return q_out, into
+    r = _binding().kv_append(cache.cfg.address(), cache.address(), cache.k.codes, cache.head_dim, cache.kv_heads, q, k, v, slots,
+                             positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out)
+    if r.__class__ is int:
+        _check("mx_kv_append", r)
+    return r
 
 
 def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengths: torch.Tensor, *,
@@ -756,49 +664,16 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengt
     sqrt(head_dim) by default.  Returns ``[S, q_heads, head_dim]`` in q's dtype unless
     ``out_dtype`` or ``out`` says otherwise, and with ``lse`` also the log sum exp, fp32
     ``[S, q_heads]``.  Scratch is allocated per call unless ``workspace`` (uint8) is given."""
-    if not q.is_cuda:
-        raise ValueError("q must be a CUDA tensor")
-    dev = q.device
-    if _elsewhere(dev, stream):
-        with _Launch(dev, stream):
+    if stream is not None:
+        with torch.cuda.stream(stream):
             return attn_decode(cache, q, page_table, lengths, scale=scale, window=window, sinks=sinks, lse=lse,
                                out_dtype=out_dtype, out=out, workspace=workspace)
-    D, S = cache.head_dim, q.shape[0]
-    if q.dtype not in _DT:
-        raise TypeError(f"unsupported dtype {q.dtype} (bf16 or fp32)")
-    _same_device(dev, "the cache", cache.k.codes, "page_table", page_table, "out", out, "workspace", workspace)
-    Hq = q.shape[1] if q.dim() == 3 else q.shape[1] // D
-    ldq = _heads(q, Hq, D, "q")
-    if page_table.dtype != torch.int32 or page_table.dim() != 2 or page_table.shape[0] != S:
-        raise ValueError(f"page_table must be int32 [{S}, max_pages]")
-    pages, (ldt, one) = page_table.shape[1], page_table.stride()
-    if (pages > 1 and one != 1) or (S > 1 and ldt < pages):
-        raise ValueError("page_table must have contiguous rows")
-    if S <= 1:
-        ldt = pages
-    pl = _vector(lengths, S, torch.int32, dev, "lengths")
-    if workspace is not None and (workspace.dtype != torch.uint8 or not workspace.is_contiguous()):
-        raise ValueError("workspace must be contiguous uint8")
-    if out is None:
-        out = q.new_empty((S, Hq, D), dtype=out_dtype)
-        if out.dtype not in _DT:
-            raise TypeError(f"unsupported dtype {out.dtype} (bf16 or fp32)")
-        ldo = Hq * D
-    elif out.dtype not in _DT or out.shape[0] != S or out.dtype != (out_dtype or out.dtype):
-        raise ValueError(f"out must have {S} rows of {out_dtype or 'bf16 or fp32'}")
-    else:
-        ldo = _heads(out, Hq, D, "out")
-    L, ref = lib(), cache.ref()
-    ls = q.new_empty((S, Hq), dtype=torch.float32) if lse else None
-    nbytes = L.mx_attn_workspace_bytes(ref, S, Hq, pages, window, sinks)
-    if workspace is None and nbytes:
-        workspace = q.new_empty(nbytes, dtype=torch.uint8)
-    rc = L.mx_attn_decode(cache.cfg.ref(), ref, q.data_ptr(), _DT[q.dtype], ldq, S, Hq, page_table.data_ptr(), ldt, pages, pl,
-                          D ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _DT[out.dtype], ldo,
-                          _p(ls), _p(workspace), 0 if workspace is None else workspace.numel(), _raw_stream(dev))
-    if rc:
-        _check("mx_attn_decode", rc)
-    return (out, ls) if lse else out
+    D = cache.head_dim
+    r = _binding().attn_decode(cache.cfg.address(), cache.address(), cache.k.codes, D, q, page_table, lengths,
+                               D ** -0.5 if scale is None else scale, window, sinks, lse, out_dtype, out, workspace)
+    if r.__class__ is int:
+        _check("mx_attn_decode", r)
+    return r
 
 
 def mbs_gemm_operand(q: Quantized, stream=None) -> Quantized:
