@@ -497,6 +497,11 @@ def dequantize(q: Quantized, out_dtype: torch.dtype = torch.float32, stream=None
     """x_hat from a ``Quantized`` (``mx_dequantize``); with a rotation the
     result is rotated back to the input space."""
     cfg = q.cfg
+    if out is None and stream is None and q.codes.is_cuda:
+        r = _binding().dequantize(q.codes, q.scales, q.tensor_scale, q.macro, q.offsets, cfg.address(), q.rows, q.cols, out_dtype)
+        if r.__class__ is int:
+            _check("mx_dequantize", r)
+        return r
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
     rc = mx_dequantize(cfg, _p(q.codes), _p(q.scales), _p(q.tensor_scale), _p(q.macro),

@@ -1,4 +1,5 @@
-// Marshalling of the decode-time operators for Python: tensors checked,
+// Marshalling of the decode-time operators, and of the dequantizer that reads
+// their cache back, for Python: tensors checked,
 // outputs allocated and the C ABI (include/mx.h) called in one step.  A decode
 // step makes such calls back to back on small tensors, where the same checks
 // written in Python took longer than the kernels.  No computation happens here.
@@ -275,6 +276,24 @@ PyObject *attn_decode(PyObject *const *a)
     return r;
 }
 
+// codes, scales, tensor_scale, macro, offsets, cfg address, rows, cols, out_dtype
+PyObject *dequantize(PyObject *const *a)
+{
+    const at::Tensor &codes = on_cuda(a[0], "codes"), &scales = tensor(a[1], "scales");
+    const at::Tensor *ts = maybe(a[2], "tensor_scale"), *macro = maybe(a[3], "macro"), *offsets = maybe(a[4], "offsets");
+    const mx_config *cfg = address<mx_config>(a[5]);
+    const int64_t rows = integer(a[6], "rows"), cols = integer(a[7], "cols");
+    const at::ScalarType s = wanted(a[8], nullptr, at::kFloat);
+    const int32_t od = dtype_code(s, "the result");
+    const c10::Device dev = codes.device();
+    const c10::cuda::CUDAGuard guard(dev);
+    at::Tensor out = at::empty({rows, cols}, codes.options().dtype(s));
+    const int rc = mx_dequantize(cfg, codes.data_ptr(), static_cast<uint8_t *>(scales.data_ptr()), static_cast<float *>(ptr(ts)),
+                                 static_cast<uint8_t *>(ptr(macro)), static_cast<uint16_t *>(ptr(offsets)), rows, cols, out.data_ptr(),
+                                 od, stream_of(dev));
+    return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
+}
+
 template <PyObject *(*F)(PyObject *const *), int N> PyObject *call(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     HANDLE_TH_ERRORS
@@ -292,7 +311,8 @@ template <PyObject *(*F)(PyObject *const *), int N> PyObject *call(PyObject *, P
 }
 
 #define MX_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {MX_METHOD(gemv, 12), MX_METHOD(kv_append, 17), MX_METHOD(attn_decode, 14), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {MX_METHOD(gemv, 12), MX_METHOD(kv_append, 17), MX_METHOD(attn_decode, 14), MX_METHOD(dequantize, 9),
+                         {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mx_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -10,6 +10,7 @@
 #include <float.h>
 #include <stdint.h>
 
+#include "mma_decode.cuh"
 #include "mx_device.cuh"
 #include "mx_internal.h"
 
@@ -330,6 +331,84 @@ int launch_dequant_oct(const DParams &p, cudaStream_t st)
     return e == cudaSuccess ? 0 : -1;
 }
 
+// The other element types, symmetric, row axis, no macro scale or rotation
+// (reading back a 6-bit or INT4 key-value cache): an octet a thread as above,
+// codes through f16, where every grid is exact.
+template <bool OUT32>
+__global__ void __launch_bounds__(kThreads) k_dequant_row8(const DParams p, const FastDiv opr_div, uint32_t noct)
+{
+    constexpr int U = 4;
+    const uint32_t T = gridDim.x * blockDim.x;
+    pdl_trigger();
+    pdl_wait();
+    const float sT = (p.ts_mode != TS_NONE && p.tensor_scale) ? *p.tensor_scale : 1.0f;
+    const bool nearest = p.sd.fmt != S_E8M0 && p.sd.rule == R_NEAREST;
+    const int lb = __ffs(p.block) - 1;
+    const uint32_t opr = (uint32_t)p.cols >> 3, S = (uint32_t)p.cols >> lb;
+    const bool six = p.ed.code_bits == 6;
+    for (uint32_t o0 = blockIdx.x * blockDim.x + threadIdx.x; o0 < noct; o0 += U * T) {
+        uint2 w[U];
+        uint32_t sc[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t o = o0 + u * T;
+            w[u] = make_uint2(0u, 0u);
+            sc[u] = 0;
+            if (o < noct) {
+                if (six) w[u] = __ldg(static_cast<const uint2 *>(p.codes) + o);
+                else w[u].x = __ldg(static_cast<const uint32_t *>(p.codes) + o);
+                if (!p.sf_gemm) {
+                    sc[u] = __ldg(p.scales + (o >> (lb - 3)));
+                } else {
+                    const uint32_t row = fast_div(o, opr_div), col = (o - row * opr) << 3;
+                    sc[u] = __ldg(p.scales + sf_chunk_index(row, col >> lb, S));
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t o = o0 + u * T;
+            if (o >= noct) break;
+            uint32_t h[4];
+            if (six) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint16_t c = (uint16_t)((k < 2 ? w[u].x : w[u].y) >> (16 * (k & 1)));
+                    if (p.ed.elem == E2M3) asm("cvt.rn.f16x2.e2m3x2 %0, %1;" : "=r"(h[k]) : "h"(c));
+                    else asm("cvt.rn.f16x2.e3m2x2 %0, %1;" : "=r"(h[k]) : "h"(c));
+                }
+            } else if (p.ed.elem == E3M0) {
+                codes8_halves<GE_E3M0>(w[u].x, h);
+            } else {
+                codes8_halves<GE_INT4>(w[u].x, h);
+            }
+            const float s = scale_value_fast(p.sd, sc[u]);
+            float v[8];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float2 q = __half22float2(*reinterpret_cast<const __half2 *>(&h[k]));
+                float2 t = __fmul2_rn(q, make_float2(s, s));
+                if (nearest) t = __fmul2_rn(t, make_float2(sT, sT));
+                v[2 * k] = s != s ? qnan() : t.x;
+                v[2 * k + 1] = s != s ? qnan() : t.y;
+            }
+            if (OUT32) {
+                float4 *dst = reinterpret_cast<float4 *>(static_cast<float *>(p.out) + (size_t)o * 8);
+                dst[0] = make_float4(v[0], v[1], v[2], v[3]);
+                dst[1] = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                uint32_t t[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * k], v[2 * k + 1]);
+                    t[k] = *reinterpret_cast<uint32_t *>(&b);
+                }
+                reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out))[o] = make_uint4(t[0], t[1], t[2], t[3]);
+            }
+        }
+    }
+}
+
 // Column axis with the rotation along columns: thread = 4 columns x `block`
 // rows, rotated back in registers.
 __global__ void __launch_bounds__(kThreads) k_dequant_colhad(const DParams p)
@@ -563,6 +642,17 @@ int grid_of(K kernel, int64_t work_warps)
     if (g > kMaxPartials) g = kMaxPartials;
     return (int)g;
 }
+
+int launch_dequant_row8(const DParams &p, cudaStream_t st)
+{
+    const uint64_t noct = (uint64_t)(p.rows * p.cols / 8);
+    const FastDiv f = make_fast_div((uint32_t)(p.cols / 8));
+    const int64_t warps = (int64_t)(noct / 4 + 255) / 256 * 8;
+    cudaError_t e;
+    if (p.out_fp32) e = launch_pdl(k_dequant_row8<true>, grid_of(k_dequant_row8<true>, warps), kThreads, 0, st, p, f, (uint32_t)noct);
+    else e = launch_pdl(k_dequant_row8<false>, grid_of(k_dequant_row8<false>, warps), kThreads, 0, st, p, f, (uint32_t)noct);
+    return e == cudaSuccess ? 0 : -1;
+}
 }  // namespace
 
 int launch_dequantize(const DParams &p, cudaStream_t st)
@@ -575,6 +665,8 @@ int launch_dequantize(const DParams &p, cudaStream_t st)
         if (p.axis == AX_ROW) return launch_dequant_oct<AX_ROW>(p, st);
         if (p.axis == AX_COL) return launch_dequant_oct<AX_COL>(p, st);
         return launch_dequant_oct<AX_2D>(p, st);
+    } else if (p.axis == AX_ROW && p.ed.elem != E2M1 && !p.asym && !p.mbs && !p.had && !(p.sf_gemm && p.ed.code_bits == 6)) {
+        return launch_dequant_row8(p, st);
     } else {
         const int64_t warps = (p.rows * p.cols / 32 + 31) / 32;
         const bool fast = p.ed.elem == E2M1 && !p.asym && !p.mbs && p.axis != AX_COL;
