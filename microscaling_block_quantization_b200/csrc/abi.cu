@@ -575,7 +575,8 @@ int64_t mx_attn_workspace_bytes(const mx_kv_cache *cache, int64_t seqs, int32_t 
                                 int32_t sinks)
 {
     if (!cache || seqs <= 0 || q_heads <= 0 || cache->kv_heads <= 0 || cache->page_size <= 0 || max_pages <= 0) return 0;
-    const int s = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks));
+    // (the most that any format's kernel splits into)
+    const int s = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks), 16);
     return s == 1 ? 0 : seqs * q_heads * s * (8 + 4 * (int64_t)cache->head_dim);
 }
 
@@ -599,7 +600,9 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     const int qs = q_dtype == MX_DT_FP32 ? 4 : 2, os = out_dtype == MX_DT_FP32 ? 4 : 2;
     if ((uintptr_t)q % qs || (uintptr_t)out % os || (uintptr_t)page_table % 4 || (uintptr_t)lengths % 4 || (uintptr_t)lse % 4)
         return MX_ERR_ALIGN;
-    const int splits = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks));
+    const int hp = q_dtype == MX_DT_FP32 || out_dtype == MX_DT_FP32;
+    const int splits = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks),
+                                   attn_warps(cache->head_dim, cfg->block, q_heads, cache->kv_heads, hp));
     if (splits > 1) {
         if (!workspace || workspace_bytes < mx_attn_workspace_bytes(cache, seqs, q_heads, max_pages, window, sinks))
             return MX_ERR_WORKSPACE;
@@ -647,7 +650,7 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     p.part_ml = reinterpret_cast<float2 *>(p.part_o + (splits > 1 ? seqs * q_heads * splits * cache->head_dim : 0));
     const int el = cfg->elem == MX_E2M1 ? GE_E2M1 : cfg->elem == MX_E3M0 ? GE_E3M0 : cfg->elem == MX_INT4 ? GE_INT4
                  : cfg->elem == MX_E2M3 ? AE_E2M3 : AE_E3M2;
-    return launch_attn(p, el, p.q_fp32 || p.o_fp32, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;
+    return launch_attn(p, el, hp, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;
 }
 
 int mx_tensor_amax(const mx_config *cfg, const void *x, int32_t x_dtype, int64_t rows, int64_t cols,

@@ -80,37 +80,44 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
     if (d == 0 && p.lse) p.lse[out] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
 }
 
-AtPick at_pick(int el, int d, int bs, int nth, int hp)
+AtPick at_pick(int el, int d, int bs, int nth, int hp, int vm)
 {
 #define AT_CASE(EL) \
-    case EL: return d == 64 ? at_kernel_##EL##_64(bs, nth, hp) : d == 128 ? at_kernel_##EL##_128(bs, nth, hp) : at_kernel_##EL##_256(bs, nth, hp);
+    case EL: return d == 64 ? at_kernel_##EL##_64(bs, nth, hp, vm) : d == 128 ? at_kernel_##EL##_128(bs, nth, hp, vm) : at_kernel_##EL##_256(bs, nth, hp, vm);
     switch (el) {
         AT_CASE(GE_E2M1)
         AT_CASE(GE_E3M0)
         AT_CASE(GE_INT4)
         AT_CASE(AE_E2M3)
-    default: return d == 64 ? at_kernel_AE_E3M2_64(bs, nth, hp) : d == 128 ? at_kernel_AE_E3M2_128(bs, nth, hp) : at_kernel_AE_E3M2_256(bs, nth, hp);
+    default: return d == 64 ? at_kernel_AE_E3M2_64(bs, nth, hp, vm) : d == 128 ? at_kernel_AE_E3M2_128(bs, nth, hp, vm) : at_kernel_AE_E3M2_256(bs, nth, hp, vm);
     }
 #undef AT_CASE
 }
 
 }  // namespace
 
-// Splits of every sequence for a call of these sizes.  The device holds about
-// 16 of the warps an SM: one sequence is split into as many stretches as run at
-// once; several, whose lengths differ, into twice as many, so that a warp
-// that is done makes room for another.  Stretches of 64 tokens at least.
-int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens)
+// Splits of every sequence for a call of these sizes.  One sequence is split
+// into as many stretches as run at once (`warps` of the kernel an SM); several,
+// whose lengths differ, into twice as many, so that a warp that is done makes
+// room for another (64 of up to 8192: 154 us, four times as many 161).
+// Stretches of 64 tokens at least.
+int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps)
 {
     const int group = q_heads / kv_heads;
     const int hg = group <= 4 ? 1 : (group + 7) / 8;
     const int64_t rows = seqs * kv_heads * hg;
     if (rows <= 0) return 1;
-    const int64_t want = (int64_t)device_sm_count() * (seqs == 1 ? 16 : 32);
+    const int64_t want = (int64_t)device_sm_count() * warps * (seqs == 1 ? 1 : 2);
     int64_t s = want / rows;
     const int64_t cap = (most_tokens + 63) / 64;
     s = s < cap ? s : cap;
     return s < 1 ? 1 : s > kAttnMaxSplits ? kAttnMaxSplits : (int)s;
+}
+
+// Warps of the call's kernel that an SM holds, by its registers.
+int attn_warps(int head_dim, int block, int q_heads, int kv_heads, int hp)
+{
+    return hp || q_heads / kv_heads > 4 || head_dim == 256 || block == 16 ? 12 : 16;
 }
 
 int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
@@ -119,7 +126,7 @@ int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
     const int nth = p.group <= 4 ? 1 : 2;
     p.head_groups = (p.group + 4 * nth - 1) / (4 * nth);
     p.tasks = p.seqs * p.splits * p.head_groups * p.kv_heads;
-    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp);
+    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp, p.sfmt == S_UE4M3);
     if (k.smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(k.k), k.smem)) return 1;
     const int64_t ctas = (p.tasks + kAtWarps - 1) / kAtWarps;
     if (launch_pdl(k.k, (unsigned)ctas, kAtThreads, k.smem, st, p) != cudaSuccess) return 1;

@@ -27,6 +27,9 @@
 //   p_t(h) where e = r, else 0: code pairs enter the instruction as decoded,
 //   nothing is transposed, and each m16 tile is one 32-block of the head, so
 //   that the block's scale multiplies the weight: w = p s_b, in binary32.
+// * E4M3 scales with E2M1 codes (NVFP4; VM = 1) need no such folding: the
+//   product of code and scale is an f16 exactly, so the codes are scaled as
+//   they are decoded, on the FMA pipe, and w is p alone.
 // * w as f16: scaled by 2^7 and, per 32-block, by a reference exponent of the
 //   block scales that also moves rarely, so w stays in [0, 2^15]; a weight is
 //   flushed only below 2^-32 of its block's largest.  One f16 rounding
@@ -196,25 +199,32 @@ template <int EL, int D, int BS> __device__ __forceinline__ uint32_t at_value_la
 // A token's scales -> binary32, one per 32-block (two with blocks of 16).
 template <int EL, int D, int BS>
 __device__ __forceinline__ void at_scales(const AttnParams &p, uint32_t area, int tok, uint32_t shifts, const uint32_t sel[2],
-                                          float *s)
+                                          const float *m, float *s)
 {
+    // (m: a power of two per 32-block)
     using G = AtGeom<EL, D, BS>;
     const uint32_t a = area + tok * G::SW;
     if (BS == 16) {
 #pragma unroll
-        for (int i = 0; i < G::SW / 4; ++i) scales4(p.sfmt, lds32(a + 4 * i), s + 4 * i);
+        for (int i = 0; i < G::SW / 4; ++i) {
+            const float f[4] = {m[2 * i], m[2 * i], m[2 * i + 1], m[2 * i + 1]};
+            scales4_times(p.sfmt, lds32(a + 4 * i), f, s + 4 * i);
+        }
         return;
     }
+    float f4[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f4[i] = i < G::NB ? m[i < G::NB ? i : 0] : 1.0f;
     uint32_t w0 = lds32(a), w1 = 0u;
     if (G::SW > 4) w1 = lds32(a + 4);
     if (G::NARROW) w0 >>= shifts;
     float f[4];
-    scales4(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[0]) : w0, f);
+    scales4_times(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[0]) : w0, f4, f);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
         if (i < G::NB) s[i] = f[i];
     if (G::NB > 4) {
-        scales4(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[1]) : w1, f);
+        scales4_times(p.sfmt, BS == 64 ? __byte_perm(w0, w1, sel[1]) : w1, f4 + 4, f);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             if (4 + i < G::NB) s[4 + i] = f[i];
@@ -262,13 +272,40 @@ __device__ __forceinline__ void at_visible(const AttnParams &p, int b, int &n, i
     }
 }
 
+// f16 pairs (s, s) of the scales of value blocks (E4M3): SUB of 32-block j
+template <int EL, int D, int BS>
+__device__ __forceinline__ void at_scales_half(uint32_t area, int tok, uint32_t shifts, uint32_t *s)
+{
+    using G = AtGeom<EL, D, BS>;
+    const uint32_t a = area + tok * G::SW;
+#pragma unroll
+    for (int i = 0; i < G::SW / 4; ++i) {
+        uint32_t w = lds32(a + 4 * i);
+        if (G::NARROW) w >>= shifts;
+        const uint32_t top = w & 0x80808080u;   // (no finite scale has the sign bit: NaN)
+        if (top) w |= (top >> 7) * 0x7fu;
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+        constexpr int N = G::NB * (BS == 16 ? 2 : 1);
+        if (4 * i < N) s[4 * i] = __byte_perm(lo, lo, 0x1010u);
+        if (4 * i + 1 < N) s[4 * i + 1] = __byte_perm(lo, lo, 0x3232u);
+        if (4 * i + 2 < N) s[4 * i + 2] = __byte_perm(hi, hi, 0x1010u);
+        if (4 * i + 3 < N) s[4 * i + 3] = __byte_perm(hi, hi, 0x3232u);
+    }
+}
+
 // NTH: groups of four heads (1 or 2); HP: binary32 precision (two pieces of
-// queries and weights)
-template <int EL, int D, int BS, int NTH, int HP>
-__global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4) k_attn(const __grid_constant__ AttnParams p)
+// queries and weights); VM: value codes scaled as f16 (E2M1 with E4M3 scales)
+template <int EL, int D, int BS, int NTH, int HP, int VM>
+__global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS == 16 ? 3 : 4) k_attn(const __grid_constant__ AttnParams p)
 {
     using G = AtGeom<EL, D, BS>;
     constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
+    constexpr int PB = VM ? 10 : 7;           // the weights' f16 exponent
     extern __shared__ __align__(256) uint8_t smem_at[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -427,7 +464,7 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
     float acc[NTH][NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        cb[j] = 0.0f;                         // (none yet)
+        cb[j] = VM ? 1.0f : 0.0f;             // (none yet)
 #pragma unroll
         for (int q = 0; q < NTH; ++q)
 #pragma unroll
@@ -450,9 +487,11 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
         // scores of tokens g, g + 8 (heads 2t, 2t + 1)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         {
-            float kl[NB * SUB], kg[NB * SUB];
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g, shift_of(g), sel, kl);
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, shift_of(g + 8), sel, kg);
+            float kl[NB * SUB], kg[NB * SUB], one[NB];
+#pragma unroll
+            for (int j = 0; j < NB; ++j) one[j] = 1.0f;
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g, shift_of(g), sel, one, kl);
+            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, shift_of(g + 8), sel, one, kg);
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint32_t lo[4], hi[4];
@@ -524,21 +563,21 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
         l0 += s[0] + s[2];
         l1 += s[1] + s[3];
 
-        // value scales of tokens t, t + 4, t + 8, t + 12
         float vs[4][NB * SUB];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, vs[i]);
-        // a scale past 2^3 times its block's reference, or none yet: the codes
-        // of scales order like their values, so each lane compares its share of
-        // the tile's scale bytes
+        if constexpr (VM == 0) {
+        // A value scale past 2^3 times its block's reference, or no reference
+        // yet?  The codes of scales order like their values, so each lane
+        // compares its share of the tile's scale bytes with the limits' codes.
         bool past = false;
         if (G::NARROW) {
-            float top = 0.0f;
+            past = cb[0] == 0.0f;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                float x[NB * SUB];
+                at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, x);
 #pragma unroll
-                for (int j = 0; j < NB * SUB; ++j) top = fmaxf(top, __fmul_rn(vs[i][j], cb[j / SUB]));
-            past = top > 8.0f || cb[0] == 0.0f;
+                for (int j = 0; j < NB * SUB; ++j) past |= x[j] > 8.0f;
+            }
         } else {
             const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
 #pragma unroll
@@ -549,17 +588,25 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
             }
         }
         if (__any_sync(0xffffffffu, past)) {
+            float x[NB], one[NB];
 #pragma unroll
             for (int j = 0; j < NB; ++j) {
-                float x = 0.0f;
+                x[j] = 0.0f;
+                one[j] = 1.0f;
+            }
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                float y[NB * SUB];
+                at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, one, y);
 #pragma unroll
-                    for (int u = 0; u < SUB; ++u) x = fmaxf(x, vs[i][j * SUB + u]);
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                for (int j = 0; j < NB * SUB; ++j) x[j / SUB] = fmaxf(x[j / SUB], y[j]);
+            }
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
+                x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
                 // 2^-floor(log2 x), within 2^-100 .. 2^100
-                const int e = min(max((int)(__float_as_uint(x) >> 23) - 127, -100), 100);
+                const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, -100), 100);
                 const float c = exp2i(-e);
                 if (cb[j] == 0.0f || c < cb[j]) {
                     const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
@@ -588,7 +635,11 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
                 }
             }
         }
-        // weights p of the lane's tokens and column head, times 2^7
+        // value scales of tokens t, t + 4, t + 8, t + 12 over the references
+#pragma unroll
+        for (int i = 0; i < 4; ++i) at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, vs[i]);
+        }
+        // weights p of the lane's tokens and column head, times 2^PB
         float pw[NTH][4];
 #pragma unroll
         for (int q = 0; q < NTH; ++q) {
@@ -598,11 +649,27 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
             for (int i = 0; i < 2; ++i) {
                 const float x0 = __shfl_sync(0xffffffffu, s[0], (t + 4 * i) * 4 + src), x1 = __shfl_sync(0xffffffffu, s[1], (t + 4 * i) * 4 + src);
                 const float y0 = __shfl_sync(0xffffffffu, s[2], (t + 4 * i) * 4 + src), y1 = __shfl_sync(0xffffffffu, s[3], (t + 4 * i) * 4 + src);
-                pw[q][i] = __fmul_rn(odd ? x1 : x0, 128.0f);
-                pw[q][2 + i] = __fmul_rn(odd ? y1 : y0, 128.0f);
+                pw[q][i] = __fmul_rn(odd ? x1 : x0, (float)(1 << PB));
+                pw[q][2 + i] = __fmul_rn(odd ? y1 : y0, (float)(1 << PB));
             }
         }
-        const uint32_t par = (g & 1) ? 0xffff0000u : 0x0000ffffu;   // the column's parity
+        const uint32_t par = (g & 1) ? 0x3c000000u : 0x00003c00u;   // the column's parity: (1, 0) or (0, 1)
+        uint32_t wv[NTH][PC][4], vh[4][NB * SUB];   // (VM)
+        if constexpr (VM) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                at_scales_half<EL, D, BS>(st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), vh[i]);
+#pragma unroll
+                for (int q = 0; q < NTH; ++q) {
+                    const uint32_t h = half2_of(pw[q][i]);
+                    wv[q][0][i] = hmul2_u(h, par);
+                    if (HP) {
+                        const float back = __low2float(*reinterpret_cast<const __half2 *>(&h));
+                        wv[q][PC - 1][i] = hmul2_u(half2_of(__fmul_rn(__fsub_rn(pw[q][i], back), 2048.0f)), par);
+                    }
+                }
+            }
+        }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t lo[4], hi[4];
@@ -610,6 +677,26 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
             at_value_codes<EL, D, BS, 1>(st + v_lane, j, g, lo[1], hi[1]);
             at_value_codes<EL, D, BS, 2>(st + v_lane, j, g, lo[2], hi[2]);
             at_value_codes<EL, D, BS, 3>(st + v_lane, j, g, lo[3], hi[3]);
+            if constexpr (VM) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    lo[i] = hmul2_u(lo[i], vh[i][j * SUB]);
+                    hi[i] = hmul2_u(hi[i], vh[i][j * SUB + SUB - 1]);
+                }
+#pragma unroll
+                for (int q = 0; q < NTH; ++q) {
+                    mma_16816(acc[q][j], lo[0], hi[0], lo[1], hi[1], wv[q][0][0], wv[q][0][1]);
+                    mma_16816(acc[q][j], lo[2], hi[2], lo[3], hi[3], wv[q][0][2], wv[q][0][3]);
+                    if (HP) {
+                        float e[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        mma_16816(e, lo[0], hi[0], lo[1], hi[1], wv[q][PC - 1][0], wv[q][PC - 1][1]);
+                        mma_16816(e, lo[2], hi[2], lo[3], hi[3], wv[q][PC - 1][2], wv[q][PC - 1][3]);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) acc[q][j][i] = fmaf(e[i], 0x1p-11f, acc[q][j][i]);
+                    }
+                }
+                continue;
+            }
 #pragma unroll
             for (int q = 0; q < NTH; ++q)
 #pragma unroll
@@ -617,12 +704,12 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
                     uint32_t w[PC][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float x = __fmul_rn(__fmul_rn(pw[q][i], cb[j]), vs[i][j * SUB + u]);
+                        const float x = __fmul_rn(pw[q][i], vs[i][j * SUB + u]);
                         const uint32_t h = half2_of(x);
-                        w[0][i] = h & par;
+                        w[0][i] = hmul2_u(h, par);   // (on the FMA pipe: the integer pipe is the busy one)
                         if (HP) {
                             const float back = __low2float(*reinterpret_cast<const __half2 *>(&h));
-                            w[PC - 1][i] = half2_of(__fmul_rn(__fsub_rn(x, back), 2048.0f)) & par;
+                            w[PC - 1][i] = hmul2_u(half2_of(__fmul_rn(__fsub_rn(x, back), 2048.0f)), par);
                         }
                     }
                     // blocks of 16: rows below 8 are the first half's pairs,
@@ -677,8 +764,8 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            // 2^(E - 7) of the block, the tensor scale, the sum
-            const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - 7 - (int)(__float_as_uint(cb[j]) >> 23)), vts);
+            // 2^(E - PB) of the block, the tensor scale, the sum
+            const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - PB - (int)(__float_as_uint(cb[j]) >> 23)), vts);
             float o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = div == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(acc[q][j][i], f), div);
@@ -705,19 +792,22 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 ? 3 : 4
 typedef void (*AtKernel)(const AttnParams);
 struct AtPick { AtKernel k; int smem; };
 
-template <int EL, int D, int BS> AtPick at_pick_nth(int nth, int hp)
+template <int EL, int D, int BS, int VM> AtPick at_pick_nth(int nth, int hp)
 {
     const int smem = kAtWarps * AtGeom<EL, D, BS>::STAGES * AtGeom<EL, D, BS>::STAGE;
-    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1> : k_attn<EL, D, BS, 1, 0>, smem};
-    return {hp ? k_attn<EL, D, BS, 2, 1> : k_attn<EL, D, BS, 2, 0>, smem};
+    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1, VM> : k_attn<EL, D, BS, 1, 0, VM>, smem};
+    return {hp ? k_attn<EL, D, BS, 2, 1, VM> : k_attn<EL, D, BS, 2, 0, VM>, smem};
 }
-template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp)
+// bs: 16, 32, or 64 for blocks of 64 and 128; vm: E4M3 scales
+template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp, int vm)
 {
-    return bs == 16 ? at_pick_nth<EL, D, 16>(nth, hp) : bs == 32 ? at_pick_nth<EL, D, 32>(nth, hp) : at_pick_nth<EL, D, 64>(nth, hp);
+    if constexpr (EL == GE_E2M1)
+        if (vm && bs < 64) return bs == 16 ? at_pick_nth<EL, D, 16, 1>(nth, hp) : at_pick_nth<EL, D, 32, 1>(nth, hp);
+    return bs == 16 ? at_pick_nth<EL, D, 16, 0>(nth, hp) : bs == 32 ? at_pick_nth<EL, D, 32, 0>(nth, hp) : at_pick_nth<EL, D, 64, 0>(nth, hp);
 }
 
 // the kernels of one element kind and head length, in translation units of their own
-#define AT_DECLARE(EL, D) AtPick at_kernel_##EL##_##D(int bs, int nth, int hp);
+#define AT_DECLARE(EL, D) AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int vm);
 #define AT_DECLARE3(EL) AT_DECLARE(EL, 64) AT_DECLARE(EL, 128) AT_DECLARE(EL, 256)
 AT_DECLARE3(GE_E2M1)
 AT_DECLARE3(GE_E3M0)
@@ -727,6 +817,6 @@ AT_DECLARE3(AE_E3M2)
 #undef AT_DECLARE3
 #undef AT_DECLARE
 #define AT_DEFINE(EL, D) \
-    AtPick at_kernel_##EL##_##D(int bs, int nth, int hp) { return at_pick_bs<EL, D>(bs, nth, hp); }
+    AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int vm) { return at_pick_bs<EL, D>(bs, nth, hp, vm); }
 
 }  // namespace mxk

@@ -125,6 +125,41 @@ __device__ __forceinline__ void scales4(int fmt, uint32_t w, float s[4])
     for (int i = 0; i < 4; ++i) s[i] = scale1(fmt, (w >> (8 * i)) & 0xffu);
 }
 
+// Four codes of a word, each times a power of two m[i] (a bf16): the E8M0
+// codes' bf16 values enter a mixed-precision multiply-add (exact), which
+// widens and scales at once on the FMA pipe.
+__device__ __forceinline__ float bf16_mul_f32(uint32_t pair, int high, float m)
+{
+    float r;
+    const uint32_t mb = __float_as_uint(m) >> 16;
+    if (high)
+        asm("{\n\t.reg .b16 a, b, c;\n\tmov.b32 {a, b}, %1;\n\tcvt.u16.u32 c, %2;\n\tfma.rn.f32.bf16 %0, b, c, 0f80000000;\n\t}"
+            : "=f"(r) : "r"(pair), "r"(mb));
+    else
+        asm("{\n\t.reg .b16 a, b, c;\n\tmov.b32 {a, b}, %1;\n\tcvt.u16.u32 c, %2;\n\tfma.rn.f32.bf16 %0, a, c, 0f80000000;\n\t}"
+            : "=f"(r) : "r"(pair), "r"(mb));
+    return r;
+}
+__device__ __forceinline__ void scales4_times(int fmt, uint32_t w, const float m[4], float s[4])
+{
+    if (fmt == S_E8M0) {
+        uint32_t lo, hi;
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.bf16x2.ue8m0x2 %0, a;\n\t"
+            "cvt.rn.bf16x2.ue8m0x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(w));
+        s[0] = bf16_mul_f32(lo, 0, m[0]);
+        s[1] = bf16_mul_f32(lo, 1, m[1]);
+        s[2] = bf16_mul_f32(hi, 0, m[2]);
+        s[3] = bf16_mul_f32(hi, 1, m[3]);
+        return;
+    }
+    scales4(fmt, w, s);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s[i] = __fmul_rn(s[i], m[i]);
+}
+
 // D (16 x 8, binary32) += A (16 x 16, f16) B (16 x 8, f16); lane = 4 g + t
 // holds A rows g, g + 8 at k = 2t, 2t + 1 (a0, a1) and 2t + 8, 2t + 9 (a2,
 // a3), B column g at the same k, D rows g, g + 8 at columns 2t, 2t + 1.

@@ -173,7 +173,8 @@ int cached_occupancy(const void *kernel, int threads, size_t smem);
 // per (kernel, device); 0 on success.
 int raise_smem_limit(const void *kernel, int bytes);
 int launch_gemv(GvParams p, cudaStream_t st);
-int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens);
+int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps);
+int attn_warps(int head_dim, int block, int q_heads, int kv_heads, int hp);
 int launch_attn(AttnParams p, int el, int hp, cudaStream_t st);
 int launch_kv_append(KvAppendParams p, int head_dim, int in_fp32, cudaStream_t st);
 
