@@ -593,6 +593,7 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     if (max_pages < 0 || max_pages > INT32_MAX || max_pages * cache->page_size > INT32_MAX || window < 0 || sinks < 0)
         return MX_ERR_INVALID;
     if (!(scale > -INFINITY && scale < INFINITY)) return MX_ERR_INVALID;
+    if (seqs * q_heads > INT32_MAX) return MX_ERR_INVALID;   // the launch grids
     if (seqs == 0) return MX_OK;
     const int64_t cols = (int64_t)q_heads * cache->head_dim;
     if (!q || !out || !lengths || (max_pages && !page_table)) return MX_ERR_INVALID;

@@ -120,6 +120,12 @@ void *vector(const at::Tensor *t, int64_t n, at::ScalarType s, c10::Device d, co
         value_error(std::string(name) + " must be " + std::to_string(n) + " contiguous " + c10::toString(s) + " on " + d.str());
     return t->data_ptr();
 }
+// a contiguous buffer of at least n bytes
+void buffer(const at::Tensor *t, int64_t n, const char *name)
+{
+    if (t && ((int64_t)t->nbytes() < n || !t->is_contiguous()))
+        value_error(std::string(name) + " must be contiguous and hold " + std::to_string(n) + " bytes");
+}
 void *stream_of(c10::Device d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 
 // x, codes, scales, tensor_scale, macro, offsets, cfg address, uses tensor scale, N, K, out_dtype, out
@@ -143,6 +149,14 @@ PyObject *gemv(PyObject *const *a)
     same_device(out, dev, "out");
     if (!PyObject_IsTrue(a[7])) ts = nullptr;
     same_device(ts, dev, "tensor_scale");
+    if (N >= 0 && K >= 0 && cfg->block > 0 && (K == 0 || N < (INT64_C(1) << 32) / K)) {
+        const int64_t blocks = N * (K / cfg->block);
+        buffer(&codes, N * K / 2, "codes");
+        buffer(&scales, blocks, "scales");
+        buffer(macro, cfg->macro_block ? N * (K / 128) : 0, "macro");
+        buffer(offsets, cfg->asymmetric ? 2 * blocks : 0, "offsets");
+        buffer(ts, 4, "tensor_scale");
+    }
     const at::ScalarType ys = wanted(a[10], out, x.scalar_type());
     const int32_t yd = dtype_code(ys, "the result");
     const c10::cuda::CUDAGuard guard(dev);
@@ -284,6 +298,9 @@ PyObject *dequantize(PyObject *const *a)
     const mx_config *cfg = address<mx_config>(a[5]);
     const int64_t rows = integer(a[6], "rows"), cols = integer(a[7], "cols");
     const at::ScalarType s = wanted(a[8], nullptr, at::kFloat);
+    same_device(&scales, codes.device(), "scales");
+    same_device(macro, codes.device(), "macro");
+    same_device(offsets, codes.device(), "offsets");
     const int32_t od = dtype_code(s, "the result");
     const c10::Device dev = codes.device();
     const c10::cuda::CUDAGuard guard(dev);

@@ -149,6 +149,7 @@ def test_attention_caches(mx, args, rc):
 
 
 @pytest.mark.parametrize("args,rc", [
+    (dict(S=1 << 20, Hq=4096, ldq=1 << 20, ldo=1 << 20), -1),
     (dict(qd=2), -1), (dict(od=3), -1), (dict(S=-1), -1), (dict(S=(1 << 20) + 1), -1), (dict(Hq=0), -1), (dict(Hq=3), -1),
     (dict(mp=-1), -1), (dict(mp=1 << 28, ldt=1 << 28), -1), (dict(win=-1), -1), (dict(sinks=-2), -1),
     (dict(scale=float("nan")), -1), (dict(scale=float("inf")), -1),

@@ -282,3 +282,29 @@ def test_no_sequences_and_no_pages(mx):
     assert mx.attn_decode(c, q[:0], table[:0], lengths[:0]).shape == (0, 2, 64)
     out, lse = mx.attn_decode(c, q, table[:, :0], lengths, lse=True)
     assert bool((out == 0).all()) and bool((lse == -math.inf).all())
+
+
+def test_refusals_of_the_binding(mx):
+    c, q, table, lengths = make(mx, mx.MXFP4, [50, 70], 4, 2, 64, 16, torch.bfloat16)
+    good = dict(q=q, page_table=table, lengths=lengths)
+    call = lambda **k: mx.attn_decode(c, **{**good, **k})  # noqa: E731
+    for k in (dict(q=q.cpu()), dict(q=q[..., :32]), dict(q=q[0]), dict(page_table=table.long()), dict(page_table=table[:1]),
+              dict(page_table=table.cpu()), dict(page_table=table.T.contiguous().T), dict(lengths=lengths.long()), dict(lengths=lengths[:1]),
+              dict(out=torch.zeros(1, 4, 64, device="cuda")), dict(out=torch.zeros(2, 4, 64)), dict(workspace=torch.zeros(9, device="cuda")),
+              dict(out=torch.zeros(2, 4, 64, device="cuda"), out_dtype=torch.bfloat16), dict(window=1 << 40)):
+        with pytest.raises(ValueError):
+            call(**k)
+    for k in (dict(q=q.half()), dict(scale="x"), dict(out_dtype=torch.float16), dict(lengths=None), dict(window=1.5)):
+        with pytest.raises(TypeError):
+            call(**k)
+    for k in (dict(window=-1), dict(sinks=-1), dict(scale=math.inf), dict(q=torch.zeros(2, 3, 64, dtype=torch.bfloat16, device="cuda"))):
+        with pytest.raises(mx.MXError) as e:
+            call(**k)
+        assert e.value.code == -1
+    c, q, table, lengths = make(mx, mx.MXFP4, [3000], 4, 2, 64, 16, torch.bfloat16)
+    with pytest.raises(mx.MXError) as e:
+        mx.attn_decode(c, q, table, lengths, workspace=torch.zeros(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.code == -5
+    n = mx.lib().mx_attn_workspace_bytes(c.ref(), 1, 4, table.shape[1], 0, 0)
+    own = torch.full((n,), 255, dtype=torch.uint8, device="cuda")         # any contents
+    assert torch.equal(mx.attn_decode(c, q, table, lengths, workspace=own), mx.attn_decode(c, q, table, lengths))

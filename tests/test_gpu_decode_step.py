@@ -115,3 +115,39 @@ def test_captured_steps(mx):
         torch.cuda.synchronize()
         assert torch.equal(y, want[i])
     assert torch.equal(eager.cache.k.codes, captured.cache.k.codes) and torch.equal(eager.cache.v.codes, captured.cache.v.codes)
+
+
+FIRST = """
+import sys
+sys.path.insert(0, {root!r})
+import torch
+import microscaling_block_quantization_b200 as mx
+g = torch.Generator(device="cuda").manual_seed(0)
+qw = mx.quantize(torch.randn(96, 256, generator=g, device="cuda").bfloat16(), mx.NVFP4, stats=False)
+x = torch.randn(2, 256, generator=g, device="cuda").bfloat16()
+c = mx.kv_cache(8, 16, 1, 64)
+k = torch.randn(100, 64, generator=g, device="cuda").bfloat16()
+slots = torch.arange(100, device="cuda")
+q = torch.randn(1, 2, 64, generator=g, device="cuda").bfloat16()
+table, n = torch.arange(8, device="cuda", dtype=torch.int32)[None], torch.tensor([100], dtype=torch.int32, device="cuda")
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    y = mx.gemv(x, qw)
+    mx.kv_append(c, None, k, k, slots)
+    a = mx.attn_decode(c, q, table, n)
+graph.replay()
+torch.cuda.synchronize()
+assert torch.equal(y, mx.gemv(x, qw)) and torch.equal(a, mx.attn_decode(c, q, table, n)) and float(a.float().abs().sum()) > 0
+print("same")
+"""
+
+
+def test_first_calls_of_a_process_inside_a_capture(mx):
+    """Nothing that a first call sets up is forbidden while a graph is captured."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stderr[-2000:]

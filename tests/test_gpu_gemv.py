@@ -241,3 +241,31 @@ def test_empty(mx):
     assert mx.gemv(torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), qw).shape == (0, 16)
     none = mx.Quantized(mx.MXFP4, 4, 0, qw.codes, qw.scales, qw.tensor_scale, None, None, None)
     assert bool((mx.gemv(torch.empty(3, 0, device="cuda"), none) == 0).all())
+
+
+def test_refusals_of_the_binding(mx):
+    """Wrong shapes, types, strides, devices and buffers raise before any launch."""
+    qw = weights(mx, mx.MXFP4, 32, 128)
+    x = torch.zeros(2, 128, dtype=torch.bfloat16, device="cuda")
+    for bad, kind in ((x[:, :96], ValueError), (x[None], ValueError), (x.half(), TypeError), (x.cpu(), ValueError),
+                      (torch.zeros(2, 256, dtype=torch.bfloat16, device="cuda")[:, ::2], ValueError),
+                      (x[:1].expand(3, 128), ValueError), (None, TypeError)):
+        with pytest.raises(kind):
+            mx.gemv(bad, qw)
+    out = torch.zeros(2, 32, device="cuda")
+    for bad, kind in ((out[:1], ValueError), (out.half(), TypeError), (out.cpu(), ValueError), (out.T.contiguous().T, ValueError)):
+        with pytest.raises(kind):
+            mx.gemv(x, qw, out=bad)
+    with pytest.raises(ValueError):
+        mx.gemv(x, qw, torch.bfloat16, out=out)
+    with pytest.raises(TypeError):
+        mx.gemv(x, qw, torch.float16)
+    import dataclasses
+    for change in (dict(codes=qw.codes[:-16]), dict(scales=qw.scales[:-1]), dict(codes=qw.codes.cpu()), dict(rows=33),
+                   dict(codes=torch.zeros(2 * 32 * 64, dtype=torch.uint8, device="cuda")[::2])):
+        with pytest.raises(ValueError):
+            mx.gemv(x, dataclasses.replace(qw, **change))
+    with pytest.raises(mx.MXError) as e:
+        mx.gemv(x, dataclasses.replace(qw, cfg=mx.Config(hadamard=32)))
+    assert e.value.code == -2
+    assert torch.equal(mx.gemv(x, qw), torch.zeros(2, 32, dtype=torch.bfloat16, device="cuda"))

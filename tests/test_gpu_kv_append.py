@@ -247,3 +247,25 @@ def test_no_tokens(mx):
     c = cache_of(mx, mx.MXFP4, 8, 2, 64)
     q, k = mx.kv_append(c, s["q"][:0], s["k"][:0], s["v"][:0], s["slots"][:0], s["positions"][:0], inv_freq=s["inv_freq"], k_out=True)
     assert q.shape == (0, 4, 64) and k.shape == (0, 2, 64)
+
+
+def test_refusals_of_the_binding(mx):
+    s = inputs(4, 2, 1, 64, torch.bfloat16, 64)
+    c = cache_of(mx, mx.MXFP4, s["rows"], 1, 64)
+    good = dict(q=s["q"], k=s["k"], v=s["v"], slots=s["slots"], positions=s["positions"], inv_freq=s["inv_freq"])
+    call = lambda **k: mx.kv_append(c, **{**good, **k})  # noqa: E731
+    wide = torch.zeros(4, 128, dtype=torch.bfloat16, device="cuda")
+    for k in (dict(k=s["k"].cpu()), dict(v=s["v"].float()), dict(v=s["v"][:3]), dict(k=wide), dict(k=wide[:, ::2]), dict(q=s["q"].cpu()),
+              dict(slots=s["slots"].int()), dict(slots=s["slots"][:3]), dict(slots=s["slots"].cpu()), dict(positions=None),
+              dict(positions=s["positions"].int()), dict(inv_freq=s["inv_freq"].double()), dict(q_gain=torch.ones(63, device="cuda")),
+              dict(k_gain=torch.ones(64, dtype=torch.bfloat16, device="cuda")), dict(q_out=s["q"].float()), dict(k_out=s["v"][:3]),
+              dict(v=s["v"][:1].expand(4, 64))):
+        with pytest.raises(ValueError):
+            call(**k)
+    for k in (dict(k=s["k"].half(), v=s["v"].half(), q=s["q"].half()), dict(k=None), dict(eps="x"), dict(k_out=3)):
+        with pytest.raises(TypeError):
+            call(**k)
+    with pytest.raises(mx.MXError) as e:
+        call(inv_freq=torch.ones(12, device="cuda"))         # 24 rotated elements
+    assert e.value.code == -2
+    check_cache(mx, c, s["k"], "k", torch.full_like(s["slots"], -1))    # nothing was written
