@@ -434,7 +434,8 @@ int mx_mbs_gemm_scales(const mx_config *cfg, const uint8_t *scales, const uint8_
  *                (ldy >= N); must not overlap an input.
  * Products q x are exact and summed in binary32, one sum per block times its
  * scale; every output is rounded once, and its value does not depend on
- * timing.  x values of a 128-column chunk below 2^-31 of the chunk's largest
+ * timing.  A chunk's sums are formed with its x scaled to 2^14 .. 2^15, and
+ * pass binary32 where weights pass about 2^100.  x values of a 128-column chunk below 2^-31 of the chunk's largest
  * are rounded at 2^-39 of it (binary32 x: at 2^-50).  An infinite or NaN x
  * gives what IEEE sums of the products give; a NaN scale a NaN.
  * 0 <= M <= 2^17; the weights are read once per 16 rows of bf16 x (8 of
@@ -517,7 +518,9 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
  *   workspace    mx_attn_workspace_bytes() bytes, 16-byte aligned, not
  *                initialised; calls that may run at the same time need their own.
  * Scores, softmax statistics and sums are binary32; the weights are rounded to
- * 11 bits for bf16 results and to 22 when q or out is fp32.  One launch, two
+ * 11 bits for bf16 results and to 22 when q or out is fp32.  Values may reach
+ * the ends of binary32; a score's sum is formed with the head's queries scaled
+ * to 2^14 .. 2^15, and passes binary32 where keys pass about 2^100.  One launch, two
  * where sequences are split; the split goes by the sizes given on the host,
  * so results do not depend on timing.
  */

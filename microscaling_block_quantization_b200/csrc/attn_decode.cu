@@ -12,8 +12,8 @@ namespace {
 
 constexpr int kJoinCols = 64;   // elements of a head a join CTA takes
 
-// One CTA per (sequence, query head, 64 elements of the head): the splits'
-// sums brought to the common maximum and added in a fixed order.  Groups of 16
+// One CTA per (sequence, query head, 64 elements of the head): the stretches'
+// results weighted by their sums at the common maximum, added in a fixed order.  Groups of 16
 // threads hold the 64 elements and take every (threads / 16)-th split; the
 // groups' sums meet in shared memory.  Every warp finds the common maximum and
 // sum of weights by itself, so that one barrier is all.
@@ -38,12 +38,9 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
     // a stretch without a visible token has m = -inf, l = 0; one whose scores
     // are NaN makes the result NaN
-    const auto weight = [m](float2 x) { return x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : exp2f(x.x - m); };
+    const auto weight = [m](float2 x) { return x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : x.y * exp2f(x.x - m); };
     float l = 0.0f;
-    for (int s = lane; s < used; s += 32) {
-        const float2 x = ml[s];
-        l = fmaf(weight(x), x.y, l);
-    }
+    for (int s = lane; s < used; s += 32) l += weight(ml[s]);
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

@@ -35,8 +35,8 @@
 //   flushed only below 2^-32 of its block's largest.  One f16 rounding
 //   (2^-11) per weight for bf16 results; for binary32 a second piece holds
 //   the rounding's remainder (2^-22).
-// * Partial results (unnormalised sums, m, l) of a sequence's stretches meet
-//   in a second launch, in order.
+// * Partial results (each stretch's own attention, m, l) of a sequence's
+//   stretches meet in a second launch, in order.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -605,8 +605,8 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
             for (int j = 0; j < NB; ++j) {
                 x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
                 x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
-                // 2^-floor(log2 x), within 2^-100 .. 2^100
-                const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, -100), 100);
+                // 2^-floor(log2 x), itself and 2^(E - PB) normal numbers
+                const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, PB - 126), 126);
                 const float c = exp2i(-e);
                 if (cb[j] == 0.0f || c < cb[j]) {
                     const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
@@ -756,8 +756,9 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
         if (head >= hn) continue;
         const int64_t out = (int64_t)seq * p.q_heads + h0 + head;
         const bool whole = p.splits == 1;
-        // of no tokens: zeros; else over the sum (a join divides later)
-        const float div = !whole ? 1.0f : l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+        // over the sum (a stretch's too, whose sum of large values might pass
+        // binary32); of no tokens: zeros
+        const float div = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
         if (g == 0) {
             if (!whole) p.part_ml[out * p.splits + split] = make_float2(m, l);
             else if (p.lse) p.lse[out] = l > 0.0f || l != l ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
@@ -768,7 +769,7 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
             const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - PB - (int)(__float_as_uint(cb[j]) >> 23)), vts);
             float o[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = div == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(acc[q][j][i], f), div);
+            for (int i = 0; i < 4; ++i) o[i] = div == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(acc[q][j][i], div), f);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int d = 32 * j + (BS == 16 ? 2 * g + 16 * i : 4 * g + 2 * i);

@@ -183,6 +183,19 @@ def test_large_and_drifting_values(mx):
             run(mx, (c, q, table, lengths))
 
 
+@pytest.mark.parametrize("name", ["mxfp4", "mxfp4_b16", "mxfp4_b64", "e2m3", "int4"])
+def test_values_near_the_ends_of_the_range(mx, name):
+    """Values near the largest and the smallest binary32 numbers, in one stretch and in many: sums of them are not formed."""
+    for seqs, n in ((300, 100), (1, 5000)):
+        c, q, table, lengths = make(mx, configs(mx)[name], [n] * seqs, 4, 2, 128, 16, torch.float32)
+        x = torch.randn(c.pages * c.page_size, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+        for gain in (2.0 ** 122, 2.0 ** -118):
+            z = mx.quantize((x * gain).bfloat16(), c.cfg, stats=False)
+            c.v.codes.copy_(z.codes)
+            c.v.scales.copy_(z.scales)
+            run(mx, (c, q, table, lengths))
+
+
 def test_scales_differ_between_blocks(mx):
     """One block of the head far larger than the others: the small ones keep their relative accuracy."""
     c, q, table, lengths = make(mx, mx.MXFP4, [200], 4, 1, 128, 16, torch.float32)
