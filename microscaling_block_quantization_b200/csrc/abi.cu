@@ -576,8 +576,12 @@ int64_t mx_attn_workspace_bytes(const mx_kv_cache *cache, int64_t seqs, int32_t 
 {
     if (!cache || seqs <= 0 || q_heads <= 0 || cache->kv_heads <= 0 || cache->page_size <= 0 || max_pages <= 0) return 0;
     // (the most that any format's kernel splits into)
-    const int s = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks), 16);
-    return s == 1 ? 0 : seqs * q_heads * s * (8 + 4 * (int64_t)cache->head_dim);
+    int64_t most = 0;
+    for (const int warps : {12, 16}) {
+        const AttnPlan plan = attn_plan(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks), warps);
+        if (!plan.joined && plan.splits > 1 && plan.splits > most) most = plan.splits;
+    }
+    return seqs * q_heads * most * (8 + 4 * (int64_t)cache->head_dim);
 }
 
 int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q, int32_t q_dtype, int64_t ldq,
@@ -602,9 +606,10 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     if ((uintptr_t)q % qs || (uintptr_t)out % os || (uintptr_t)page_table % 4 || (uintptr_t)lengths % 4 || (uintptr_t)lse % 4)
         return MX_ERR_ALIGN;
     const int hp = q_dtype == MX_DT_FP32 || out_dtype == MX_DT_FP32;
-    const int splits = attn_splits(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks),
-                                   attn_warps(cache->head_dim, cfg->block, q_heads, cache->kv_heads, hp));
-    if (splits > 1) {
+    const AttnPlan plan = attn_plan(seqs, cache->kv_heads, q_heads, attn_most(cache, max_pages, window, sinks),
+                                    attn_warps(cache->head_dim, cfg->block, q_heads, cache->kv_heads, hp));
+    const bool parts = plan.splits > 1 && !plan.joined;   // results of the splits in the workspace
+    if (parts) {
         if (!workspace || workspace_bytes < mx_attn_workspace_bytes(cache, seqs, q_heads, max_pages, window, sinks))
             return MX_ERR_WORKSPACE;
         if (!aligned16(workspace)) return MX_ERR_ALIGN;
@@ -646,9 +651,11 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     p.ldo = ldo;
     p.o_fp32 = out_dtype == MX_DT_FP32;
     p.lse = lse;
-    p.splits = splits;
+    p.splits = plan.splits;
+    p.joined = plan.joined;
+    p.warps = plan.warps;
     p.part_o = static_cast<float *>(workspace);
-    p.part_ml = reinterpret_cast<float2 *>(p.part_o + (splits > 1 ? seqs * q_heads * splits * cache->head_dim : 0));
+    p.part_ml = reinterpret_cast<float2 *>(p.part_o + (parts ? seqs * q_heads * plan.splits * cache->head_dim : 0));
     const int el = cfg->elem == MX_E2M1 ? GE_E2M1 : cfg->elem == MX_E3M0 ? GE_E3M0 : cfg->elem == MX_INT4 ? GE_INT4
                  : cfg->elem == MX_E2M3 ? AE_E2M3 : AE_E3M2;
     return launch_attn(p, el, hp, static_cast<cudaStream_t>(stream)) ? MX_ERR_CUDA : MX_OK;

@@ -10,6 +10,7 @@ namespace mxk {
 
 namespace {
 
+constexpr int kAttnSmem = 227 * 1024;
 constexpr int kJoinCols = 64;   // elements of a head a join CTA takes
 
 // One CTA per (sequence, query head, 64 elements of the head): the stretches'
@@ -36,18 +37,15 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
     for (int s = lane; s < used; s += 32) m = fmaxf(m, ml[s].x);
 #pragma unroll
     for (int x = 16; x; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    // a stretch without a visible token has m = -inf, l = 0; one whose scores
-    // are NaN makes the result NaN
-    const auto weight = [m](float2 x) { return x.y == 0.0f ? 0.0f : x.y != x.y ? x.y : x.y * exp2f(x.x - m); };
     float l = 0.0f;
-    for (int s = lane; s < used; s += 32) l += weight(ml[s]);
+    for (int s = lane; s < used; s += 32) l += at_weight(ml[s], m);
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float *part = p.part_o + out * p.splits * D + d;
 #pragma unroll 4
     for (int s = grp; s < used; s += groups) {
-        const float w = weight(ml[s]);
+        const float w = at_weight(ml[s], m);
         const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * D);
         o.x = fmaf(w, v.x, o.x);
         o.y = fmaf(w, v.y, o.y);
@@ -64,17 +62,8 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
         o.z += v.z;
         o.w += v.w;
     }
-    const bool any = l > 0.0f || l != l;
-    const float inv = any ? __fdiv_rn(1.0f, l) : 0.0f;
     const float v[4] = {o.x, o.y, o.z, o.w};
-    const int64_t at = (int64_t)seq * p.ldo + (int64_t)head * D + d;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float y = any ? __fmul_rn(v[i], inv) : 0.0f;
-        if (p.o_fp32) static_cast<float *>(p.out)[at + i] = y;
-        else static_cast<__nv_bfloat16 *>(p.out)[at + i] = __float2bfloat16_rn(y);
-    }
-    if (d == 0 && p.lse) p.lse[out] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
+    at_store4(p, seq, head, d, m, l, v);
 }
 
 AtPick at_pick(int el, int d, int bs, int nth, int hp, int vm)
@@ -93,22 +82,47 @@ AtPick at_pick(int el, int d, int bs, int nth, int hp, int vm)
 
 }  // namespace
 
-// Splits of every sequence for a call of these sizes.  One sequence is split
-// into as many stretches as run at once (`warps` of the kernel an SM); several,
-// whose lengths differ, into twice as many, so that a warp that is done makes
-// room for another (64 of up to 8192: 154 us, four times as many 161).
-// Stretches of 64 tokens at least.
-int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps)
+// How a call of these sizes is split (times on a B200, 32 query and 8 key heads
+// of 128, MXFP4 unless said).  As many stretches of 32 tokens at least as run at
+// once (`warps_sm` warps of the kernel an SM); where several long sequences give
+// stretches of 256 tokens and more, twice as many, so that a warp that is done
+// makes room for another: 64 sequences of up to 8192 tokens 176 -> 156 us, but
+// 256 of up to 300 33 -> 39 us.
+// A second launch that joins the stretches costs 3 to 5 us.  Where there are
+// CTAs for half the SMs and more, a CTA's warps are a sequence's stretches and
+// join them: 16 x 1000 15.3 -> 12.4 us, NVFP4 64 x 1000 42 -> 37 us, 128 x 2048 92 -> 85
+// us.  With fewer CTAs, warps that share few SMs lose more than the launch costs
+// (8 x 8192 31 against 44 us, clusters of CTAs included), but for up to 4 stretches
+// of 64 tokens (1 x 200 8.5 -> 7.5 us); stretches past 512 tokens are better off as
+// tasks of their own (64 x 8192 156 against 162 us).
+AttnPlan attn_plan(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps_sm)
 {
     const int group = q_heads / kv_heads;
     const int hg = group <= 4 ? 1 : (group + 7) / 8;
-    const int64_t rows = seqs * kv_heads * hg;
-    if (rows <= 0) return 1;
-    const int64_t want = (int64_t)device_sm_count() * warps * (seqs == 1 ? 1 : 2);
-    int64_t s = want / rows;
-    const int64_t cap = (most_tokens + 63) / 64;
-    s = s < cap ? s : cap;
-    return s < 1 ? 1 : s > kAttnMaxSplits ? kAttnMaxSplits : (int)s;
+    const int64_t rows = seqs * kv_heads * hg, sms = device_sm_count();
+    AttnPlan plan = {1, 0, kAtWarps};
+    if (rows <= 0) return plan;
+    if (2 * rows < sms && most_tokens <= 256) {
+        plan.splits = most_tokens <= 64 ? 1 : (int)((most_tokens + 63) / 64);
+        plan.joined = plan.splits > 1;
+        if (plan.joined) plan.warps = plan.splits;
+        return plan;
+    }
+    const int64_t once = sms * warps_sm / rows, twice = 2 * sms * warps_sm / rows, most = (most_tokens + 31) / 32;
+    int64_t s = once < most ? once : most;
+    if (seqs > 1 && twice > 1 && most_tokens >= 256 * twice) s = twice;
+    if (s < 2) return plan;
+    int w = (int)(s < warps_sm ? s : warps_sm);
+    if (2 * rows >= sms && most_tokens <= 512 * w) {
+        // more CTAs than SMs: so many warps each that an SM's warps divide by them
+        while (rows > sms && warps_sm % w) --w;
+        plan.splits = plan.warps = w;
+        plan.joined = w > 1;
+        if (!plan.joined) plan.warps = kAtWarps;
+        return plan;
+    }
+    plan.splits = s > kAttnMaxSplits ? kAttnMaxSplits : (int)s;
+    return plan;
 }
 
 // Warps of the call's kernel that an SM holds, by its registers.
@@ -122,12 +136,15 @@ int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
     p.group = p.q_heads / p.kv_heads;
     const int nth = p.group <= 4 ? 1 : 2;
     p.head_groups = (p.group + 4 * nth - 1) / (4 * nth);
-    p.tasks = p.seqs * p.splits * p.head_groups * p.kv_heads;
     const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp, p.sfmt == S_UE4M3);
-    if (k.smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(k.k), k.smem)) return 1;
-    const int64_t ctas = (p.tasks + kAtWarps - 1) / kAtWarps;
-    if (launch_pdl(k.k, (unsigned)ctas, kAtThreads, k.smem, st, p) != cudaSuccess) return 1;
-    if (p.splits == 1) return 0;
+    // (the rings of 8-bit codes of long heads leave room for fewer warps)
+    while (p.warps * k.ring > kAttnSmem) p.warps = p.splits = p.warps - 1;
+    const int smem = p.warps * k.ring;
+    p.tasks = p.seqs * (p.joined ? 1 : p.splits) * p.head_groups * p.kv_heads;
+    if (smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(k.k), kAttnSmem)) return 1;
+    const int64_t ctas = p.joined ? p.tasks : (p.tasks + p.warps - 1) / p.warps;
+    if (launch_pdl(k.k, (unsigned)ctas, p.warps * 32, smem, st, p) != cudaSuccess) return 1;
+    if (p.splits == 1 || p.joined) return 0;
     int groups = 4;
     while (groups < 32 && groups < p.splits) groups *= 2;
     return launch_pdl(k_attn_join, (unsigned)(p.seqs * p.q_heads * (p.head_dim / kJoinCols)), groups * 16, 0, st, p) == cudaSuccess ? 0 : 1;

@@ -36,7 +36,8 @@
 //   (2^-11) per weight for bf16 results; for binary32 a second piece holds
 //   the rounding's remainder (2^-22).
 // * Partial results (each stretch's own attention, m, l) of a sequence's
-//   stretches meet in a second launch, in order.
+//   stretches meet in a fixed order: where a CTA's warps hold them all, in
+//   shared memory at the end of the kernel, else in a second launch.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -50,8 +51,9 @@ namespace mxk {
 // element kinds: the 4-bit ones of GE_*, then one code per byte
 enum { AE_E2M3 = 4, AE_E3M2 = 5 };
 
-constexpr int kAtWarps = 4;
-constexpr int kAtThreads = kAtWarps * 32;
+constexpr int kAtWarps = 4;   // of a CTA whose warps are not joined
+// warps of an SM, and the most of a CTA: 128 or 168 registers a thread
+template <int D, int BS, int NTH, int HP> __host__ __device__ constexpr int at_warps() { return HP || NTH == 2 || D == 256 || BS == 16 ? 12 : 16; }
 
 template <int EL, int D, int BS> struct AtGeom {
     static constexpr int BITS = EL >= AE_E2M3 ? 8 : 4;
@@ -272,6 +274,27 @@ __device__ __forceinline__ void at_visible(const AttnParams &p, int b, int &n, i
     }
 }
 
+// The weight of a stretch's result (m, l) at the common maximum: one without a
+// visible token has m = -inf, l = 0; one whose scores are NaN makes the result NaN.
+__device__ __forceinline__ float at_weight(float2 ml, float m)
+{
+    return ml.y == 0.0f ? 0.0f : ml.y != ml.y ? ml.y : ml.y * exp2f(ml.x - m);
+}
+// Four elements of a head, o the weighted sum and l the sum of weights.
+__device__ __forceinline__ void at_store4(const AttnParams &p, int seq, int head, int d, float m, float l, const float o[4])
+{
+    const bool any = l > 0.0f || l != l;
+    const float inv = any ? __fdiv_rn(1.0f, l) : 0.0f;
+    const int64_t at = (int64_t)seq * p.ldo + (int64_t)head * p.head_dim + d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float y = any ? __fmul_rn(o[i], inv) : 0.0f;
+        if (p.o_fp32) static_cast<float *>(p.out)[at + i] = y;
+        else static_cast<__nv_bfloat16 *>(p.out)[at + i] = __float2bfloat16_rn(y);
+    }
+    if (d == 0 && p.lse) p.lse[(int64_t)seq * p.q_heads + head] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
+}
+
 // f16 pairs (s, s) of the scales of value blocks (E4M3): SUB of 32-block j
 template <int EL, int D, int BS>
 __device__ __forceinline__ void at_scales_half(uint32_t area, int tok, uint32_t shifts, uint32_t *s)
@@ -301,7 +324,7 @@ __device__ __forceinline__ void at_scales_half(uint32_t area, int tok, uint32_t 
 // NTH: groups of four heads (1 or 2); HP: binary32 precision (two pieces of
 // queries and weights); VM: value codes scaled as f16 (E2M1 with E4M3 scales)
 template <int EL, int D, int BS, int NTH, int HP, int VM>
-__global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS == 16 ? 3 : 4) k_attn(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(const __grid_constant__ AttnParams p)
 {
     using G = AtGeom<EL, D, BS>;
     constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
@@ -312,21 +335,25 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
     pdl_trigger();
     pdl_wait();
 
-    // the warp's task: key head fastest, then head group, split, sequence
-    int64_t task = (int64_t)blockIdx.x * kAtWarps + warp;
+    // the warp's task: key head fastest, then head group, split, sequence; the
+    // warps of a joined CTA are the splits
+    const int warps = blockDim.x >> 5;
+    int64_t task = p.joined ? (int64_t)blockIdx.x : (int64_t)blockIdx.x * warps + warp;
     if (task >= p.tasks) return;
     const int kh = (int)(task % p.kv_heads);
     task /= p.kv_heads;
     const int hg = (int)(task % p.head_groups);
     task /= p.head_groups;
-    const int split = (int)(task % p.splits), seq = (int)(task / p.splits);
+    const int split = p.joined ? warp : (int)(task % p.splits);
+    const int seq = (int)(p.joined ? task : task / p.splits);
     const int h0 = kh * p.group + hg * (4 * NTH);           // first query head
     const int hn = min(4 * NTH, p.group - hg * (4 * NTH));  // heads of this task
     int n, vis, sinks;
     at_visible(p, seq, n, vis, sinks);
     const int tiles = (vis + 15) >> 4, per = (tiles + p.splits - 1) / p.splits;
     const int tile0 = split * per, tile1 = min(tile0 + per, tiles);
-    if (tile0 >= tile1 && p.splits > 1) return;   // (the join reads no more than the splits in use)
+    // (the join's launch reads no more than the splits in use)
+    if (tile0 >= tile1 && p.splits > 1 && !p.joined) return;
 
     const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_at) + warp * G::STAGES * G::STAGE;
     const int skip = n - vis;                 // tokens between the sinks and the window
@@ -747,6 +774,10 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
         l1 += __shfl_xor_sync(0xffffffffu, l1, d);
     }
     const float vts = p.v_ts ? *p.v_ts : 1.0f;
+    // a joined CTA's results, in the warps' own rings: 4 NTH heads, then (m, l) of each
+    float *mine = reinterpret_cast<float *>(smem_at + warp * G::STAGES * G::STAGE);
+    static_assert(4 * NTH * (D + 2) * 4 <= G::STAGES * G::STAGE, "a warp's results fit its ring");
+    __syncwarp();                             // the ring is read
 #pragma unroll
     for (int q = 0; q < NTH; ++q) {
         const int src = (t >> 1) + 2 * q, head = t + 4 * q;
@@ -760,7 +791,8 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
         // binary32); of no tokens: zeros
         const float div = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
         if (g == 0) {
-            if (!whole) p.part_ml[out * p.splits + split] = make_float2(m, l);
+            if (p.joined) *reinterpret_cast<float2 *>(mine + 4 * NTH * D + 2 * head) = make_float2(m, l);
+            else if (!whole) p.part_ml[out * p.splits + split] = make_float2(m, l);
             else if (p.lse) p.lse[out] = l > 0.0f || l != l ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
         }
 #pragma unroll
@@ -773,7 +805,9 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int d = 32 * j + (BS == 16 ? 2 * g + 16 * i : 4 * g + 2 * i);
-                if (!whole) {
+                if (p.joined) {
+                    *reinterpret_cast<float2 *>(mine + head * D + d) = make_float2(o[2 * i], o[2 * i + 1]);
+                } else if (!whole) {
                     *reinterpret_cast<float2 *>(p.part_o + (out * p.splits + split) * D + d) = make_float2(o[2 * i], o[2 * i + 1]);
                 } else {
                     const int64_t at = (int64_t)seq * p.ldo + (int64_t)(h0 + head) * D + d;
@@ -788,16 +822,52 @@ __global__ void __launch_bounds__(kAtThreads, HP || NTH == 2 || D == 256 || BS =
             }
         }
     }
+    if (!p.joined) return;
+
+    // The join of a CTA's warps, at the common maximum: a lane takes four
+    // elements of a head, or of more than four splits every fourth (four lanes,
+    // whose sums are added).
+    __syncthreads();
+    const int items = hn * (D / 4), share = p.splits > 4 ? 2 : 0, step = 1 << share, sub = lane & (step - 1);
+    for (int i0 = split * (32 >> share); i0 < items; i0 += p.splits * (32 >> share)) {
+        const int item = i0 + (lane >> share), head = min(item / (D / 4), hn - 1), d = 4 * (item & (D / 4 - 1));
+        float m = -INFINITY;
+#pragma unroll 4
+        for (int s = sub; s < p.splits; s += step) {
+            const float *r = reinterpret_cast<const float *>(smem_at + s * G::STAGES * G::STAGE);
+            m = fmaxf(m, r[4 * NTH * D + 2 * head]);
+        }
+        for (int x = 1; x < step; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+        float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+        for (int s = sub; s < p.splits; s += step) {
+            const float *r = reinterpret_cast<const float *>(smem_at + s * G::STAGES * G::STAGE);
+            const float w = at_weight(*reinterpret_cast<const float2 *>(r + 4 * NTH * D + 2 * head), m);
+            const float4 v = *reinterpret_cast<const float4 *>(r + head * D + d);
+            l += w;
+            o[0] = fmaf(w, v.x, o[0]);
+            o[1] = fmaf(w, v.y, o[1]);
+            o[2] = fmaf(w, v.z, o[2]);
+            o[3] = fmaf(w, v.w, o[3]);
+        }
+        __syncwarp();
+        for (int x = 1; x < step; x <<= 1) {
+            l += __shfl_xor_sync(0xffffffffu, l, x);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], x);
+        }
+        if (sub == 0 && item < items) at_store4(p, seq, h0 + head, d, m, l, o);
+    }
 }
 
 typedef void (*AtKernel)(const AttnParams);
-struct AtPick { AtKernel k; int smem; };
+struct AtPick { AtKernel k; int ring; };   // ring: bytes of a warp
 
 template <int EL, int D, int BS, int VM> AtPick at_pick_nth(int nth, int hp)
 {
-    const int smem = kAtWarps * AtGeom<EL, D, BS>::STAGES * AtGeom<EL, D, BS>::STAGE;
-    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1, VM> : k_attn<EL, D, BS, 1, 0, VM>, smem};
-    return {hp ? k_attn<EL, D, BS, 2, 1, VM> : k_attn<EL, D, BS, 2, 0, VM>, smem};
+    const int ring = AtGeom<EL, D, BS>::STAGES * AtGeom<EL, D, BS>::STAGE;
+    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1, VM> : k_attn<EL, D, BS, 1, 0, VM>, ring};
+    return {hp ? k_attn<EL, D, BS, 2, 1, VM> : k_attn<EL, D, BS, 2, 0, VM>, ring};
 }
 // bs: 16, 32, or 64 for blocks of 64 and 128; vm: E4M3 scales
 template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp, int vm)

@@ -148,10 +148,12 @@ struct AttnParams {
     int o_fp32;
     float *lse;
     int splits;
+    int joined;              // a CTA's warps are the splits, and join their results
+    int warps;               // of a CTA
     float2 *part_ml;         // [seqs][q_heads][splits]: reference, sum
     float *part_o;           // [seqs][q_heads][splits][head_dim]
     int group, head_groups;  // query heads per key head; warps per key head (set by the launch)
-    int64_t tasks;
+    int64_t tasks;           // of a warp; joined: of a CTA
 };
 
 // per-launch helpers implemented in the .cu files
@@ -173,7 +175,13 @@ int cached_occupancy(const void *kernel, int threads, size_t smem);
 // per (kernel, device); 0 on success.
 int raise_smem_limit(const void *kernel, int bytes);
 int launch_gemv(GvParams p, cudaStream_t st);
-int attn_splits(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps);
+// How mx_attn_decode's work is split.
+struct AttnPlan {
+    int splits;    // of a sequence
+    int joined;    // the warps of a CTA are the splits and join their results; else a second launch does
+    int warps;     // of a CTA
+};
+AttnPlan attn_plan(int64_t seqs, int kv_heads, int q_heads, int64_t most_tokens, int warps_sm);
 int attn_warps(int head_dim, int block, int q_heads, int kv_heads, int hp);
 int launch_attn(AttnParams p, int el, int hp, cudaStream_t st);
 int launch_kv_append(KvAppendParams p, int head_dim, int in_fp32, cudaStream_t st);

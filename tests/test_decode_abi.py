@@ -168,7 +168,9 @@ def test_attention_workspace_size(mx):
     c = cache(mx, pages=1 << 12, page_size=64, dim=128)
     assert L.mx_attn_workspace_bytes(c, 0, 4, 10, 0, 0) == 0 and L.mx_attn_workspace_bytes(None, 1, 4, 10, 0, 0) == 0
     assert L.mx_attn_workspace_bytes(c, 1, 4, 1, 0, 0) == 0                       # one page: not split
-    long, short = L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 0, 0), L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 500, 4)
+    long, short = L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 0, 0), L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 5000, 4)
+    assert L.mx_attn_workspace_bytes(c, 1, 4, 1 << 12, 200, 4) == 0               # joined within a CTA
+    assert L.mx_attn_workspace_bytes(c, 128, 4, 16, 0, 0) == 0
     assert long > short > 0 and long % (4 * (8 + 512)) == 0
 
 
