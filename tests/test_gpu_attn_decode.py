@@ -144,6 +144,23 @@ def test_split_sequences(mx, name, seqs, n):
     run(mx, make(mx, configs(mx)[name], lengths, 8, 2, 128, 64, torch.float32, qgain=2.0))
 
 
+@pytest.mark.parametrize("Hq,H,name", [(4, 1, "mxfp4"), (14, 2, "nvfp4"), (9, 1, "e2m3")])
+def test_ragged_batches(mx, Hq, H, name):
+    """Long, short and empty sequences of one batch; batches shorter than the table allows."""
+    for dtype in (torch.bfloat16, torch.float32):
+        for lengths in ([9000, 0, 1, 16, 8000, 17, 0, 0, 5000, 33], [0, 0, 6000], [6000, 0, 0], [1] * 40 + [9000] + [100] * 40,
+                        [40000, 3], [700, 2900] * 20):
+            c, q, table, ls = make(mx, configs(mx)[name], lengths, Hq, H, 64, 64, dtype)
+            run(mx, (c, q, table, ls))
+            run(mx, (c, q, table, ls), window=300, sinks=5)
+            run(mx, (c, q, table, ls.clamp(max=20)))     # fewer tiles than splits
+            run(mx, (c, q, table, ls * 0))
+            out = mx.attn_decode(c, q, table, ls)
+            for b in (0, len(lengths) - 1):              # as each sequence by itself, but for the order of the sums
+                one = mx.attn_decode(c, q[b:b + 1], table[b:b + 1], ls[b:b + 1])
+                assert bool((out[b] - one[0]).abs().max() <= 0.02 * one.abs().max())
+
+
 @pytest.mark.parametrize("window,sinks", [(1, 0), (16, 4), (100, 1), (50, 1000), (1000, 4), (7, 0), (33, 17)])
 def test_window_and_sinks(mx, window, sinks):
     run(mx, make(mx, mx.MXFP4, [0, 1, 5, 40, 116, 117, 500, 2000], 4, 2, 64, 16, torch.float32), window=window, sinks=sinks)
