@@ -520,9 +520,9 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
  * Scores, softmax statistics and sums are binary32; the weights are rounded to
  * 11 bits for bf16 results and to 22 when q or out is fp32.  Values may reach
  * the ends of binary32; a score's sum is formed with the head's queries scaled
- * to 2^14 .. 2^15, and passes binary32 where keys pass about 2^100.  One launch, two
- * where sequences are split over several CTAs; the split goes by the sizes given on the host,
- * so results do not depend on timing.
+ * to 2^14 .. 2^15, and passes binary32 where keys pass about 2^100.  One launch,
+ * two where sequences are split over several CTAs; the split goes by the sizes
+ * given on the host, so results do not depend on timing.
  */
 int64_t mx_attn_workspace_bytes(const mx_kv_cache *cache, int64_t seqs, int32_t q_heads, int64_t max_pages, int32_t window,
                                 int32_t sinks);

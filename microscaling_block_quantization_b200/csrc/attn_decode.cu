@@ -14,10 +14,10 @@ constexpr int kAttnSmem = 227 * 1024;
 constexpr int kJoinCols = 64;   // elements of a head a join CTA takes
 
 // One CTA per (sequence, query head, 64 elements of the head): the stretches'
-// results weighted by their sums at the common maximum, added in a fixed order.  Groups of 16
-// threads hold the 64 elements and take every (threads / 16)-th split; the
-// groups' sums meet in shared memory.  Every warp finds the common maximum and
-// sum of weights by itself, so that one barrier is all.
+// results weighted by their sums at the common maximum, added in a fixed order.
+// Groups of 16 threads hold the 64 elements and take every (threads / 16)-th
+// split; the groups' sums meet in shared memory.  Every warp finds the common
+// maximum and sum of weights by itself, so that one barrier is all.
 __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnParams p)
 {
     __shared__ float4 red[512];

@@ -86,9 +86,10 @@ int launch_gemv(GvParams p, cudaStream_t st)
     // estimate in nanoseconds from sweeps on a B200: a warp's 128-column chunk
     // takes 480 (NT = 2: 800) beside 15 others; a (chunk, token) of x 12 to
     // stage; the join reads C KS sums an output, from other CTAs at 150 against
-    // 60 each round, and a wave of partial sums more costs 1500.  4096 x 4096, one token: C, KS = 1, 8 5.6 us, 4, 4 6.9,
-    // 1, 1 9.5; 4096 x 14336 INT4, 4 tokens: 4, 2 17.5, 1, 8 25.4, 1, 1 56.7;
-    // 65536 x 8192, 16 tokens: 4, 1 107, 1, 1 131, 1, 8 285.
+    // 60 each round, and a wave of partial sums more costs 1500.  4096 x 4096,
+    // one token: C, KS = 1, 8 5.6 us, 4, 4 6.9, 1, 1 9.5; 4096 x 14336 INT4, 4
+    // tokens: 4, 2 17.5, 1, 8 25.4, 1, 1 56.7; 65536 x 8192, 16 tokens: 4, 1
+    // 107, 1, 1 131, 1, 8 285.
     GvKernel k = gv_pick(p.elem, mode, bc, nt);
     if (raise_smem_limit(reinterpret_cast<const void *>(k), kGvSmem)) return 1;
     const int toks = (int)(p.M < p.group ? p.M : p.group);
