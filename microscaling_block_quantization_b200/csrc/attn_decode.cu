@@ -66,16 +66,16 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
     at_store4(p, seq, head, d, m, l, v);
 }
 
-AtPick at_pick(int el, int d, int bs, int nth, int hp, int vm)
+AtPick at_pick(int el, int d, int bs, int nth, int hp, int sfmt)
 {
 #define AT_CASE(EL) \
-    case EL: return d == 64 ? at_kernel_##EL##_64(bs, nth, hp, vm) : d == 128 ? at_kernel_##EL##_128(bs, nth, hp, vm) : at_kernel_##EL##_256(bs, nth, hp, vm);
+    case EL: return d == 64 ? at_kernel_##EL##_64(bs, nth, hp, sfmt) : d == 128 ? at_kernel_##EL##_128(bs, nth, hp, sfmt) : at_kernel_##EL##_256(bs, nth, hp, sfmt);
     switch (el) {
         AT_CASE(GE_E2M1)
         AT_CASE(GE_E3M0)
         AT_CASE(GE_INT4)
         AT_CASE(AE_E2M3)
-    default: return d == 64 ? at_kernel_AE_E3M2_64(bs, nth, hp, vm) : d == 128 ? at_kernel_AE_E3M2_128(bs, nth, hp, vm) : at_kernel_AE_E3M2_256(bs, nth, hp, vm);
+    default: return d == 64 ? at_kernel_AE_E3M2_64(bs, nth, hp, sfmt) : d == 128 ? at_kernel_AE_E3M2_128(bs, nth, hp, sfmt) : at_kernel_AE_E3M2_256(bs, nth, hp, sfmt);
     }
 #undef AT_CASE
 }
@@ -136,7 +136,7 @@ int launch_attn(AttnParams p, int el, int hp, cudaStream_t st)
     p.group = p.q_heads / p.kv_heads;
     const int nth = p.group <= 4 ? 1 : 2;
     p.head_groups = (p.group + 4 * nth - 1) / (4 * nth);
-    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp, p.sfmt == S_UE4M3);
+    const AtPick k = at_pick(el, p.head_dim, p.log2B == 4 ? 16 : p.log2B == 5 ? 32 : 64, nth, hp, p.sfmt);
     // (the rings of 8-bit codes of long heads leave room for fewer warps)
     while (p.warps * k.ring > kAttnSmem) p.warps = p.splits = p.warps - 1;
     const int smem = p.warps * k.ring;

@@ -30,6 +30,8 @@
 // * E4M3 scales with E2M1 codes (NVFP4; VM = 1) need no such folding: the
 //   product of code and scale is an f16 exactly, so the codes are scaled as
 //   they are decoded, on the FMA pipe, and w is p alone.
+// * A tile's scale bytes are decoded once, a share a lane, and read back by all
+//   as words (64 x 8192 157 -> 138 us, 1 x 131072 NVFP4 67 -> 58 us).
 // * w as f16: scaled by 2^7 and, per 32-block, by a reference exponent of the
 //   block scales that also moves rarely, so w stays in [0, 2^15]; a weight is
 //   flushed only below 2^-32 of its block's largest.  One f16 rounding
@@ -40,10 +42,9 @@
 //   shared memory at the end of the kernel, else in a second launch.
 //
 // Measured (32 query heads, 8 key heads of 128): 64 sequences of up to 8192
-// tokens in MXFP4 157 us (2.7 TB/s), one of 131072 in NVFP4 67 us: the codes'
-// conversion and the scales keep the integer pipe at 55% and the issue slots at
-// 61% (430 instructions for 16 tokens of a key head).  One sequence of 1000
-// tokens 9.1 us: two launches, and 0.7 us for each 16 tokens of a warp.
+// tokens in MXFP4 138 us (3.1 TB/s), one of 131072 in NVFP4 58 us: bound by the
+// instructions that turn codes into operands and place the rows.  One sequence
+// of 1000 tokens 8.8 us: two launches, and 0.6 us for each 16 tokens of a warp.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -76,6 +77,8 @@ template <int EL, int D, int BS> struct AtGeom {
     // exclusive or of its address
     static constexpr int STAGE = (META_AT + 16 + ROW - 1) / ROW * ROW;
     static constexpr int STAGES = STAGE * 4 * kAtWarps <= 48 * 1024 ? 4 : 3;
+    // a tile's decoded scales: words of key scales, then of value scales
+    static constexpr int SCALES_AT = STAGES * STAGE, WARP = SCALES_AT + (NARROW ? 0 : 128 * SW);
     // piece swizzle by row: the eight rows a K read touches at once, and the
     // four of a V read, fall on different banks.  Rows 8 apart have the same,
     // and of row t + 4 i (t < 4) it is swz(t) ^ swz4(i).
@@ -111,6 +114,15 @@ template <int OFF> __device__ __forceinline__ uint32_t lds16(uint32_t a)
     uint16_t r;
     asm volatile("ld.shared.b16 %0, [%1+%2];" : "=h"(r) : "r"(a), "n"(OFF));
     return r;
+}
+
+__device__ __forceinline__ void sts64(uint32_t a, uint32_t x, uint32_t y)
+{
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(a), "r"(x), "r"(y) : "memory");
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
 }
 
 // 2^x, good to 2 ulp; results below 2^-126 are zero
@@ -301,6 +313,22 @@ __device__ __forceinline__ void at_store4(const AttnParams &p, int seq, int head
     if (d == 0 && p.lse) p.lse[(int64_t)seq * p.q_heads + head] = any ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
 }
 
+// Four E4M3 scale bytes -> their f16 pairs (s, s).
+__device__ __forceinline__ void e4m3_pairs(uint32_t w, uint32_t s[4])
+{
+    const uint32_t top = w & 0x80808080u;   // (no finite scale has the sign bit: NaN)
+    if (top) w |= (top >> 7) * 0x7fu;
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi) : "r"(w));
+    s[0] = __byte_perm(lo, lo, 0x1010u);
+    s[1] = __byte_perm(lo, lo, 0x3232u);
+    s[2] = __byte_perm(hi, hi, 0x1010u);
+    s[3] = __byte_perm(hi, hi, 0x3232u);
+}
 // f16 pairs (s, s) of the scales of value blocks (E4M3): SUB of 32-block j
 template <int EL, int D, int BS>
 __device__ __forceinline__ void at_scales_half(uint32_t area, int tok, uint32_t shifts, uint32_t *s)
@@ -311,30 +339,67 @@ __device__ __forceinline__ void at_scales_half(uint32_t area, int tok, uint32_t 
     for (int i = 0; i < G::SW / 4; ++i) {
         uint32_t w = lds32(a + 4 * i);
         if (G::NARROW) w >>= shifts;
-        const uint32_t top = w & 0x80808080u;   // (no finite scale has the sign bit: NaN)
-        if (top) w |= (top >> 7) * 0x7fu;
-        uint32_t lo, hi;
-        asm("{\n\t.reg .b16 a, b;\n\t"
-            "mov.b32 {a, b}, %2;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-            : "=r"(lo), "=r"(hi) : "r"(w));
+        uint32_t x[4];
+        e4m3_pairs(w, x);
         constexpr int N = G::NB * (BS == 16 ? 2 : 1);
-        if (4 * i < N) s[4 * i] = __byte_perm(lo, lo, 0x1010u);
-        if (4 * i + 1 < N) s[4 * i + 1] = __byte_perm(lo, lo, 0x3232u);
-        if (4 * i + 2 < N) s[4 * i + 2] = __byte_perm(hi, hi, 0x1010u);
-        if (4 * i + 3 < N) s[4 * i + 3] = __byte_perm(hi, hi, 0x3232u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (4 * i + k < N) s[4 * i + k] = x[k];
+    }
+}
+
+// The lane's share of a tile's scale bytes (SW / 2 of them, at `from`), each
+// decoded once, into words for all lanes: binary32 times m (null: 1), f16 pairs
+// of that (HALF), f16 pairs of E4M3 bytes (E4M3).
+enum { AS_F32 = 0, AS_HALF = 1, AS_E4M3 = 2 };
+template <int SW, int TO>
+__device__ __forceinline__ void at_spread_scales(int fmt, uint32_t from, uint32_t to, int lane, const float *m)
+{
+    from += lane * (SW / 2);
+    to += lane * (SW * 2);
+#pragma unroll
+    for (int i = 0; i < (SW + 7) / 8; ++i) {
+        const uint32_t w = SW == 4 ? lds16(from) : lds32(from + 4 * i);
+        uint32_t o[4];
+        if (TO == AS_E4M3) {
+            e4m3_pairs(w, o);
+        } else {
+            float f[4];
+            if (m) {
+                const float m4[4] = {m[4 * i], m[4 * i + 1], m[SW == 4 ? 0 : 4 * i + 2], m[SW == 4 ? 0 : 4 * i + 3]};
+                scales4_times(fmt, w, m4, f);
+            } else {
+                scales4(fmt, w, f);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) o[k] = TO == AS_HALF ? half2_of(f[k]) : __float_as_uint(f[k]);
+        }
+        if (SW == 4) sts64(to, o[0], o[1]);
+        else sts128(to + 16 * i, o[0], o[1], o[2], o[3]);
+    }
+}
+// A token's words.
+template <int SW> __device__ __forceinline__ void at_token_words(uint32_t area, int tok, uint32_t *w)
+{
+#pragma unroll
+    for (int i = 0; i < SW / 4; ++i) {
+        const uint4 x = lds128(area + tok * (SW * 4) + 16 * i);
+        w[4 * i] = x.x;
+        w[4 * i + 1] = x.y;
+        w[4 * i + 2] = x.z;
+        w[4 * i + 3] = x.w;
     }
 }
 
 // NTH: groups of four heads (1 or 2); HP: binary32 precision (two pieces of
-// queries and weights); VM: value codes scaled as f16 (E2M1 with E4M3 scales)
+// queries and weights); VM: 1, value codes scaled as f16 (E2M1 with E4M3 scales);
+// 2, weights scaled as f16 (E8M0 scales: powers of two, so that only the weight is rounded)
 template <int EL, int D, int BS, int NTH, int HP, int VM>
 __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(const __grid_constant__ AttnParams p)
 {
     using G = AtGeom<EL, D, BS>;
     constexpr int NB = G::NB, SUB = BS == 16 ? 2 : 1, PC = HP ? 2 : 1;
-    constexpr int PB = VM ? 10 : 7;           // the weights' f16 exponent
+    constexpr int PB = VM == 1 ? 10 : 7;           // the weights' f16 exponent
     extern __shared__ __align__(256) uint8_t smem_at[];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int g = lane >> 2, t = lane & 3;
@@ -361,7 +426,7 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
     // (the join's launch reads no more than the splits in use)
     if (tile0 >= tile1 && p.splits > 1 && !p.joined) return;
 
-    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_at) + warp * G::STAGES * G::STAGE;
+    const uint32_t ring = (uint32_t)__cvta_generic_to_shared(smem_at) + warp * G::WARP;
     const int skip = n - vis;                 // tokens between the sinks and the window
     const int32_t *table = p.table + (int64_t)seq * p.ld_table;
     const int nsc = D >> p.log2B;             // scales of a head
@@ -497,7 +562,7 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
     float acc[NTH][NB][4];
 #pragma unroll
     for (int j = 0; j < NB; ++j) {
-        cb[j] = VM ? 1.0f : 0.0f;             // (none yet)
+        cb[j] = VM == 1 ? 1.0f : 0.0f;        // (none yet)
 #pragma unroll
         for (int q = 0; q < NTH; ++q)
 #pragma unroll
@@ -506,6 +571,8 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
 
     const uint32_t k_lane = at_key_lane<EL, D, BS>(g, t), v_lane = at_value_lane<EL, D, BS>(g, t);
     uint32_t lim[(G::SW + 7) / 8] = {};       // limits of the lane's share of value scale bytes
+    float cl[(G::SW + 7) / 8 * 4] = {};       // and their blocks' 2^-E
+    const uint32_t words = ring + G::SCALES_AT;
     uint32_t st = ring;
     for (int tile = tile0; tile < tile1; ++tile) {
         cp_async_wait<G::STAGES - 2>();
@@ -517,14 +584,106 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         // where a token's scales begin in their word
         const auto shift_of = [&](int tk) { return G::NARROW ? (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8 : 0u; };
 
+        if constexpr (VM != 1) {
+            // A value scale past 2^3 times its block's reference, or no reference
+            // yet?  The codes of scales order like their values, so each lane
+            // compares its share of the tile's scale bytes with the limits' codes.
+            bool past = false;
+            if (G::NARROW) {
+                past = cb[0] == 0.0f;
+    #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x[NB * SUB];
+                    at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, x);
+    #pragma unroll
+                    for (int j = 0; j < NB * SUB; ++j) past |= x[j] > 8.0f;
+                }
+            } else {
+                const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
+    #pragma unroll
+                for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                    const uint32_t w = G::SW == 4 ? lds16(a) : lds32(a + 4 * i);
+    #pragma unroll
+                    for (int k = 0; k < (G::SW == 4 ? 2 : 4); ++k) past |= ((w >> (8 * k)) & 0xffu) > ((lim[i] >> (8 * k)) & 0xffu);
+                }
+            }
+            if (__any_sync(0xffffffffu, past)) {
+                float x[NB], one[NB];
+    #pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    x[j] = 0.0f;
+                    one[j] = 1.0f;
+                }
+    #pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float y[NB * SUB];
+                    at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, one, y);
+    #pragma unroll
+                    for (int j = 0; j < NB * SUB; ++j) x[j / SUB] = fmaxf(x[j / SUB], y[j]);
+                }
+    #pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
+                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
+                    // 2^-floor(log2 x), itself and 2^(E - PB) normal numbers
+                    const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, PB - 126), 126);
+                    const float c = exp2i(-e);
+                    if (cb[j] == 0.0f || c < cb[j]) {
+                        const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
+    #pragma unroll
+                        for (int q = 0; q < NTH; ++q)
+    #pragma unroll
+                            for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
+                        cb[j] = c;
+                    }
+                }
+                if (!G::NARROW) {
+                    // the limits of the lane's bytes: the code of 2^(E + 3)
+    #pragma unroll
+                    for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                        lim[i] = 0u;
+    #pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int at = (lane * (G::SW / 2) + 4 * i + k) & (G::SW - 1);   // the byte's scale
+                            int e = 0;
+    #pragma unroll
+                            for (int j = 0; j < NB; ++j)
+                                if (at / SUB == j) e = 127 - (int)(__float_as_uint(cb[j]) >> 23);
+                            const int code = p.sfmt == S_E8M0 ? e + 130 : (e + 3 + (p.sfmt == S_UE4M3 ? 7 : 15)) * 8;
+                            lim[i] |= (uint32_t)min(max(code, 0), 255) << (8 * k);
+                            cl[4 * i + k] = exp2i(-e);
+                        }
+                    }
+                }
+            }
+        }
+        // the tile's scales, each decoded by one lane
+        if constexpr (!G::NARROW) {
+            at_spread_scales<G::SW, AS_F32>(p.sfmt, st + G::KS_AT, words, lane, nullptr);
+            at_spread_scales<G::SW, VM == 0 ? AS_F32 : VM == 1 ? AS_E4M3 : AS_HALF>(p.sfmt, st + G::VS_AT, words + 64 * G::SW, lane, cl);
+            __syncwarp();
+        }
+
         // scores of tokens g, g + 8 (heads 2t, 2t + 1)
         float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         {
-            float kl[NB * SUB], kg[NB * SUB], one[NB];
+            float kl[NB * SUB], kg[NB * SUB];
+            if constexpr (!G::NARROW) {
+                uint32_t wl[NB * SUB], wg[NB * SUB];
+                at_token_words<G::SW>(words, g, wl);
+                at_token_words<G::SW>(words, g + 8, wg);
 #pragma unroll
-            for (int j = 0; j < NB; ++j) one[j] = 1.0f;
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g, shift_of(g), sel, one, kl);
-            at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, shift_of(g + 8), sel, one, kg);
+                for (int j = 0; j < NB * SUB; ++j) {
+                    kl[j] = bits2f(wl[j]);
+                    kg[j] = bits2f(wg[j]);
+                }
+            } else {
+                float one[NB];
+#pragma unroll
+                for (int j = 0; j < NB; ++j) one[j] = 1.0f;
+                at_scales<EL, D, BS>(p, st + G::KS_AT, g, shift_of(g), sel, one, kl);
+                at_scales<EL, D, BS>(p, st + G::KS_AT, g + 8, shift_of(g + 8), sel, one, kg);
+            }
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
                 uint32_t lo[4], hi[4];
@@ -596,81 +755,23 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         l0 += s[0] + s[2];
         l1 += s[1] + s[3];
 
-        float vs[4][NB * SUB];
-        if constexpr (VM == 0) {
-        // A value scale past 2^3 times its block's reference, or no reference
-        // yet?  The codes of scales order like their values, so each lane
-        // compares its share of the tile's scale bytes with the limits' codes.
-        bool past = false;
-        if (G::NARROW) {
-            past = cb[0] == 0.0f;
+        float vs[4][NB * SUB];                // (VM 0) value scales of tokens t, t + 4, t + 8, t + 12 over the references
+        uint32_t vh[4][NB * SUB];             // (else) as f16 pairs: the scales, or over the references
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float x[NB * SUB];
-                at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, x);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (!G::NARROW) {
+                uint32_t w[NB * SUB];
+                at_token_words<G::SW>(words + 64 * G::SW, t + 4 * i, w);
 #pragma unroll
-                for (int j = 0; j < NB * SUB; ++j) past |= x[j] > 8.0f;
-            }
-        } else {
-            const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
-#pragma unroll
-            for (int i = 0; i < (G::SW + 7) / 8; ++i) {
-                const uint32_t w = G::SW == 4 ? lds16(a) : lds32(a + 4 * i);
-#pragma unroll
-                for (int k = 0; k < (G::SW == 4 ? 2 : 4); ++k) past |= ((w >> (8 * k)) & 0xffu) > ((lim[i] >> (8 * k)) & 0xffu);
-            }
-        }
-        if (__any_sync(0xffffffffu, past)) {
-            float x[NB], one[NB];
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                x[j] = 0.0f;
-                one[j] = 1.0f;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float y[NB * SUB];
-                at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, one, y);
-#pragma unroll
-                for (int j = 0; j < NB * SUB; ++j) x[j / SUB] = fmaxf(x[j / SUB], y[j]);
-            }
-#pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
-                x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
-                // 2^-floor(log2 x), itself and 2^(E - PB) normal numbers
-                const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, PB - 126), 126);
-                const float c = exp2i(-e);
-                if (cb[j] == 0.0f || c < cb[j]) {
-                    const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
-#pragma unroll
-                    for (int q = 0; q < NTH; ++q)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
-                    cb[j] = c;
+                for (int j = 0; j < NB * SUB; ++j) {
+                    if (VM) vh[i][j] = w[j];
+                    else vs[i][j] = bits2f(w[j]);
                 }
+            } else if constexpr (VM) {
+                at_scales_half<EL, D, BS>(st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), vh[i]);
+            } else {
+                at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, vs[i]);
             }
-            if (!G::NARROW) {
-                // the limits of the lane's bytes: the code of 2^(E + 3)
-#pragma unroll
-                for (int i = 0; i < (G::SW + 7) / 8; ++i) {
-                    lim[i] = 0u;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int at = (lane * (G::SW / 2) + 4 * i + k) & (G::SW - 1);   // the byte's scale
-                        int e = 0;
-#pragma unroll
-                        for (int j = 0; j < NB; ++j)
-                            if (at / SUB == j) e = 127 - (int)(__float_as_uint(cb[j]) >> 23);
-                        const int code = p.sfmt == S_E8M0 ? e + 130 : (e + 3 + (p.sfmt == S_UE4M3 ? 7 : 15)) * 8;
-                        lim[i] |= (uint32_t)min(max(code, 0), 255) << (8 * k);
-                    }
-                }
-            }
-        }
-        // value scales of tokens t, t + 4, t + 8, t + 12 over the references
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, vs[i]);
         }
         // weights p of the lane's tokens and column head, times 2^PB
         float pw[NTH][4];
@@ -687,11 +788,10 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
             }
         }
         const uint32_t par = (g & 1) ? 0x3c000000u : 0x00003c00u;   // the column's parity: (1, 0) or (0, 1)
-        uint32_t wv[NTH][PC][4], vh[4][NB * SUB];   // (VM)
+        uint32_t wv[NTH][PC][4];              // (VM 1, 2) the weights as f16 pieces
         if constexpr (VM) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                at_scales_half<EL, D, BS>(st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), vh[i]);
+            for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int q = 0; q < NTH; ++q) {
                     const uint32_t h = half2_of(pw[q][i]);
@@ -701,7 +801,6 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                         wv[q][PC - 1][i] = hmul2_u(half2_of(__fmul_rn(__fsub_rn(pw[q][i], back), 2048.0f)), par);
                     }
                 }
-            }
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
@@ -710,7 +809,7 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
             at_value_codes<EL, D, BS, 1>(st + v_lane, j, g, lo[1], hi[1]);
             at_value_codes<EL, D, BS, 2>(st + v_lane, j, g, lo[2], hi[2]);
             at_value_codes<EL, D, BS, 3>(st + v_lane, j, g, lo[3], hi[3]);
-            if constexpr (VM) {
+            if constexpr (VM == 1) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     lo[i] = hmul2_u(lo[i], vh[i][j * SUB]);
@@ -737,6 +836,11 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                     uint32_t w[PC][4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
+                        if (VM == 2) {
+                            // (a power of two times an f16: exact but below 2^-14)
+                            w[0][i] = hmul2_u(wv[q][0][i], vh[i][j * SUB + u]);
+                            continue;
+                        }
                         const float x = __fmul_rn(pw[q][i], vs[i][j * SUB + u]);
                         const uint32_t h = half2_of(x);
                         w[0][i] = hmul2_u(h, par);   // (on the FMA pipe: the integer pipe is the busy one)
@@ -781,8 +885,8 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
     }
     const float vts = p.v_ts ? *p.v_ts : 1.0f;
     // a joined CTA's results, in the warps' own rings: 4 NTH heads, then (m, l) of each
-    float *mine = reinterpret_cast<float *>(smem_at + warp * G::STAGES * G::STAGE);
-    static_assert(4 * NTH * (D + 2) * 4 <= G::STAGES * G::STAGE, "a warp's results fit its ring");
+    float *mine = reinterpret_cast<float *>(smem_at + warp * G::WARP);
+    static_assert(4 * NTH * (D + 2) * 4 <= G::SCALES_AT, "a warp's results fit its ring");
     __syncwarp();                             // the ring is read
 #pragma unroll
     for (int q = 0; q < NTH; ++q) {
@@ -840,14 +944,14 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         float m = -INFINITY;
 #pragma unroll 4
         for (int s = sub; s < p.splits; s += step) {
-            const float *r = reinterpret_cast<const float *>(smem_at + s * G::STAGES * G::STAGE);
+            const float *r = reinterpret_cast<const float *>(smem_at + s * G::WARP);
             m = fmaxf(m, r[4 * NTH * D + 2 * head]);
         }
         for (int x = 1; x < step; x <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
         float l = 0.0f, o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
         for (int s = sub; s < p.splits; s += step) {
-            const float *r = reinterpret_cast<const float *>(smem_at + s * G::STAGES * G::STAGE);
+            const float *r = reinterpret_cast<const float *>(smem_at + s * G::WARP);
             const float w = at_weight(*reinterpret_cast<const float2 *>(r + 4 * NTH * D + 2 * head), m);
             const float4 v = *reinterpret_cast<const float4 *>(r + head * D + d);
             l += w;
@@ -871,20 +975,25 @@ struct AtPick { AtKernel k; int ring; };   // ring: bytes of a warp
 
 template <int EL, int D, int BS, int VM> AtPick at_pick_nth(int nth, int hp)
 {
-    const int ring = AtGeom<EL, D, BS>::STAGES * AtGeom<EL, D, BS>::STAGE;
-    if (nth == 1) return {hp ? k_attn<EL, D, BS, 1, 1, VM> : k_attn<EL, D, BS, 1, 0, VM>, ring};
-    return {hp ? k_attn<EL, D, BS, 2, 1, VM> : k_attn<EL, D, BS, 2, 0, VM>, ring};
+    const int ring = AtGeom<EL, D, BS>::WARP;
+    if constexpr (VM != 2) {
+        if (hp) return {nth == 1 ? k_attn<EL, D, BS, 1, 1, VM> : k_attn<EL, D, BS, 2, 1, VM>, ring};
+    }
+    return {nth == 1 ? k_attn<EL, D, BS, 1, 0, VM> : k_attn<EL, D, BS, 2, 0, VM>, ring};
 }
-// bs: 16, 32, or 64 for blocks of 64 and 128; vm: E4M3 scales
-template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp, int vm)
+// bs: 16, 32, or 64 for blocks of 64 and 128
+template <int EL, int D> AtPick at_pick_bs(int bs, int nth, int hp, int sfmt)
 {
     if constexpr (EL == GE_E2M1)
-        if (vm && bs < 64) return bs == 16 ? at_pick_nth<EL, D, 16, 1>(nth, hp) : at_pick_nth<EL, D, 32, 1>(nth, hp);
+        if (sfmt == S_UE4M3 && bs < 64) return bs == 16 ? at_pick_nth<EL, D, 16, 1>(nth, hp) : at_pick_nth<EL, D, 32, 1>(nth, hp);
+    if (sfmt == S_E8M0 && !hp && bs == 16) return at_pick_nth<EL, D, 16, 2>(nth, hp);
+    if constexpr (D >= 128)
+        if (sfmt == S_E8M0 && !hp && bs == 32) return at_pick_nth<EL, D, 32, 2>(nth, hp);
     return bs == 16 ? at_pick_nth<EL, D, 16, 0>(nth, hp) : bs == 32 ? at_pick_nth<EL, D, 32, 0>(nth, hp) : at_pick_nth<EL, D, 64, 0>(nth, hp);
 }
 
 // the kernels of one element kind and head length, in translation units of their own
-#define AT_DECLARE(EL, D) AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int vm);
+#define AT_DECLARE(EL, D) AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int sfmt);
 #define AT_DECLARE3(EL) AT_DECLARE(EL, 64) AT_DECLARE(EL, 128) AT_DECLARE(EL, 256)
 AT_DECLARE3(GE_E2M1)
 AT_DECLARE3(GE_E3M0)
@@ -894,6 +1003,6 @@ AT_DECLARE3(AE_E3M2)
 #undef AT_DECLARE3
 #undef AT_DECLARE
 #define AT_DEFINE(EL, D) \
-    AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int vm) { return at_pick_bs<EL, D>(bs, nth, hp, vm); }
+    AtPick at_kernel_##EL##_##D(int bs, int nth, int hp, int sfmt) { return at_pick_bs<EL, D>(bs, nth, hp, sfmt); }
 
 }  // namespace mxk

@@ -176,10 +176,11 @@ def test_table_entries_outside_the_cache(mx):
     run(mx, (c, q, table, lengths))
 
 
-def test_large_and_drifting_values(mx):
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_large_and_drifting_values(mx, dtype):
     """A running maximum and value scales that grow along the sequence, by far more than either margin; huge and tiny values."""
-    for D, name in ((64, "mxfp4"), (128, "mxfp4_b16"), (64, "e3m2")):
-        c, q, table, lengths = make(mx, configs(mx)[name], [600, 300], 8, 2, D, 16, torch.float32, extra=0)
+    for D, name in ((64, "mxfp4"), (128, "mxfp4"), (128, "mxfp4_b16"), (64, "e3m2"), (256, "e2m3")):
+        c, q, table, lengths = make(mx, configs(mx)[name], [600, 300], 8, 2, D, 16, dtype, extra=0)
         rows = c.pages * c.page_size
         order = torch.empty(rows, device="cuda")
         for b in range(2):
@@ -200,11 +201,12 @@ def test_large_and_drifting_values(mx):
             run(mx, (c, q, table, lengths))
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("name", ["mxfp4", "mxfp4_b16", "mxfp4_b64", "e2m3", "int4"])
-def test_values_near_the_ends_of_the_range(mx, name):
+def test_values_near_the_ends_of_the_range(mx, name, dtype):
     """Values near the largest and the smallest binary32 numbers, in one stretch and in many: sums of them are not formed."""
     for seqs, n in ((300, 100), (1, 5000)):
-        c, q, table, lengths = make(mx, configs(mx)[name], [n] * seqs, 4, 2, 128, 16, torch.float32)
+        c, q, table, lengths = make(mx, configs(mx)[name], [n] * seqs, 4, 2, 128, 16, dtype)
         x = torch.randn(c.pages * c.page_size, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
         for gain in (2.0 ** 122, 2.0 ** -118):
             z = mx.quantize((x * gain).bfloat16(), c.cfg, stats=False)
