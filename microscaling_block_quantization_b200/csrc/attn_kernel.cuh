@@ -143,10 +143,10 @@ __device__ __forceinline__ uint32_t half2_of(float x)
 template <int EL> __device__ __forceinline__ void pairs2(uint32_t c, uint32_t &lo, uint32_t &hi)
 {
     if (EL == GE_E2M1) {
-        // (each from the low byte of a register: the conversion of another
-        // byte of a value loaded in 16 bits came out wrong with nvcc 12.9)
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(lo) : "r"(c));
-        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t}" : "=r"(hi) : "r"(c >> 8));
+        // (c is no value loaded in 8 or 16 bits: of such a one, nvcc 12.9's
+        // conversion of another byte than the first came out wrong)
+        asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %2;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\tcvt.rn.f16x2.e2m1x2 %1, b1;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(c));
     } else if (EL == AE_E2M3) {
         asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e2m3x2 %0, a;\n\tcvt.rn.f16x2.e2m3x2 %1, b;\n\t}"
             : "=r"(lo), "=r"(hi) : "r"(c));
@@ -190,29 +190,50 @@ template <int EL, int D, int BS> __device__ __forceinline__ uint32_t at_key_lane
     return BS == 16 ? row + 4 * t : (row ^ ((t >> 1) << 4)) + 8 * (t & 1);
 }
 
-// Code pairs 2g, 2g + 1 (blocks of 16: g and g + 8) of 32-block b of value row
-// t + 4 I -> the operand's rows g and g + 8.  at: the lane's place in row t.
+// Code pairs 2g, 2g + 1 (blocks of 16: g and g + 8) of 32-block b of value rows
+// t + 4 I and t + 4 I + 4 -> the operand's rows g and g + 8.  at: the lane's place
+// in row t; sel: which bytes of its words the lane takes (at_value_sel).
 template <int EL, int D, int BS, int I>
-__device__ __forceinline__ void at_value_codes(uint32_t at, int b, int g, uint32_t &lo, uint32_t &hi)
+__device__ __forceinline__ void at_value_codes(uint32_t at, int b, uint32_t sel, uint32_t lo[2], uint32_t hi[2])
 {
     using G = AtGeom<EL, D, BS>;
-    constexpr int OFF = 4 * I * G::ROW;
+    constexpr int OFF = 4 * I * G::ROW, OFF2 = OFF + 4 * G::ROW;
     if constexpr (G::BITS == 4) {
-        const uint32_t p = at ^ ((b ^ G::swz4(I)) << 4);
-        // (blocks of 16: byte g of each half, read as the 16 bits around it)
-        const uint32_t w = BS == 16 ? __byte_perm(lds16<OFF>(p), lds16<OFF + 8>(p), (g & 1) ? 0x4451u : 0x4440u) : lds16<OFF>(p);
-        pairs2<EL>(w, lo, hi);
+        const uint32_t p = at ^ ((b ^ G::swz4(I)) << 4), p2 = at ^ ((b ^ G::swz4(I + 1)) << 4);
+        if constexpr (BS == 16) {
+            // byte g of each half, out of the word around it
+            const uint32_t w = __byte_perm(lds32<OFF>(p), lds32<OFF + 8>(p), sel), w2 = __byte_perm(lds32<OFF2>(p2), lds32<OFF2 + 8>(p2), sel);
+            pairs2<EL>(w, lo[0], hi[0]);
+            pairs2<EL>(w2, lo[1], hi[1]);
+        } else {
+            // two bytes of each row's word
+            const uint32_t w = __byte_perm(lds32<OFF>(p), lds32<OFF2>(p2), sel);
+            uint32_t h[4];
+            codes8_halves<EL>(w, h);
+            lo[0] = h[0];
+            hi[0] = h[1];
+            lo[1] = h[2];
+            hi[1] = h[3];
+        }
     } else {
-        const uint32_t p = at ^ (((2 * b) ^ G::swz4(I)) << 4);
-        const uint32_t w = BS == 16 ? __byte_perm(lds16<OFF>(p), lds16<OFF>(p ^ 16), 0x5410u) : lds32<OFF>(p);
-        pairs2<EL>(w, lo, hi);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint32_t p = at ^ (((2 * b) ^ G::swz4(I + k)) << 4);
+            const uint32_t w = BS == 16 ? __byte_perm(lds16<OFF>(p + k * 4 * G::ROW), lds16<OFF>((p ^ 16) + k * 4 * G::ROW), 0x5410u)
+                                        : lds32<OFF>(p + k * 4 * G::ROW);
+            pairs2<EL>(w, lo[k], hi[k]);
+        }
     }
+}
+template <int BS> __device__ __forceinline__ uint32_t at_value_sel(int g)
+{
+    return BS == 16 ? (uint32_t)((g & 3) | ((g & 3) + 4) << 4) : (g & 1) ? 0x7632u : 0x5410u;
 }
 template <int EL, int D, int BS> __device__ __forceinline__ uint32_t at_value_lane(int g, int t)
 {
     using G = AtGeom<EL, D, BS>;
     const uint32_t row = G::V_AT + t * G::ROW + (G::swz(t) << 4);
-    if (G::BITS == 4) return row + (BS == 16 ? (g & 6) : 2 * g);
+    if (G::BITS == 4) return row + (BS == 16 ? (g & 4) : 2 * (g & 6));
     return BS == 16 ? row + 2 * g : (row ^ ((g >> 2) << 4)) + 4 * (g & 3);
 }
 
@@ -569,7 +590,7 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
             for (int i = 0; i < 4; ++i) acc[q][j][i] = 0.0f;
     }
 
-    const uint32_t k_lane = at_key_lane<EL, D, BS>(g, t), v_lane = at_value_lane<EL, D, BS>(g, t);
+    const uint32_t k_lane = at_key_lane<EL, D, BS>(g, t), v_lane = at_value_lane<EL, D, BS>(g, t), v_sel = at_value_sel<BS>(g);
     uint32_t lim[(G::SW + 7) / 8] = {};       // limits of the lane's share of value scale bytes
     float cl[(G::SW + 7) / 8 * 4] = {};       // and their blocks' 2^-E
     const uint32_t words = ring + G::SCALES_AT;
@@ -805,10 +826,8 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
             uint32_t lo[4], hi[4];
-            at_value_codes<EL, D, BS, 0>(st + v_lane, j, g, lo[0], hi[0]);
-            at_value_codes<EL, D, BS, 1>(st + v_lane, j, g, lo[1], hi[1]);
-            at_value_codes<EL, D, BS, 2>(st + v_lane, j, g, lo[2], hi[2]);
-            at_value_codes<EL, D, BS, 3>(st + v_lane, j, g, lo[3], hi[3]);
+            at_value_codes<EL, D, BS, 0>(st + v_lane, j, v_sel, lo, hi);
+            at_value_codes<EL, D, BS, 2>(st + v_lane, j, v_sel, lo + 2, hi + 2);
             if constexpr (VM == 1) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {

@@ -205,7 +205,7 @@ def test_large_and_drifting_values(mx, dtype):
 @pytest.mark.parametrize("name", ["mxfp4", "mxfp4_b16", "mxfp4_b64", "e2m3", "int4"])
 def test_values_near_the_ends_of_the_range(mx, name, dtype):
     """Values near the largest and the smallest binary32 numbers, in one stretch and in many: sums of them are not formed."""
-    for seqs, n in ((300, 100), (1, 5000)):
+    for seqs, n in ((20, 40), (20, 100), (1, 5000)):
         c, q, table, lengths = make(mx, configs(mx)[name], [n] * seqs, 4, 2, 128, 16, dtype)
         x = torch.randn(c.pages * c.page_size, 256, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
         for gain in (2.0 ** 122, 2.0 ** -118):
