@@ -41,11 +41,12 @@ __global__ void __launch_bounds__(512) k_attn_join(const __grid_constant__ AttnP
     for (int s = lane; s < used; s += 32) l += at_weight(ml[s], m);
 #pragma unroll
     for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const float inv = at_over(l);             // (weights of 1 at most: no sum passes binary32)
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     const float *part = p.part_o + out * p.splits * D + d;
 #pragma unroll 4
     for (int s = grp; s < used; s += groups) {
-        const float w = at_weight(ml[s], m);
+        const float w = __fmul_rn(at_weight(ml[s], m), inv);
         const float4 v = *reinterpret_cast<const float4 *>(part + (int64_t)s * D);
         o.x = fmaf(w, v.x, o.x);
         o.y = fmaf(w, v.y, o.y);

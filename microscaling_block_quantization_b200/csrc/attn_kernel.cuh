@@ -319,15 +319,16 @@ __device__ __forceinline__ float at_weight(float2 ml, float m)
 {
     return ml.y == 0.0f ? 0.0f : ml.y != ml.y ? ml.y : ml.y * exp2f(ml.x - m);
 }
-// Four elements of a head, o the weighted sum and l the sum of weights.
+// Over the sum of the weights: nothing where there are none.
+__device__ __forceinline__ float at_over(float l) { return l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f; }
+// Four elements of a head; l: the sum of weights at the maximum m.
 __device__ __forceinline__ void at_store4(const AttnParams &p, int seq, int head, int d, float m, float l, const float o[4])
 {
     const bool any = l > 0.0f || l != l;
-    const float inv = any ? __fdiv_rn(1.0f, l) : 0.0f;
     const int64_t at = (int64_t)seq * p.ldo + (int64_t)head * p.head_dim + d;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float y = any ? __fmul_rn(o[i], inv) : 0.0f;
+        const float y = any ? o[i] : 0.0f;
         if (p.o_fp32) static_cast<float *>(p.out)[at + i] = y;
         else static_cast<__nv_bfloat16 *>(p.out)[at + i] = __float2bfloat16_rn(y);
     }
@@ -646,8 +647,8 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                 for (int j = 0; j < NB; ++j) {
                     x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
                     x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
-                    // 2^-floor(log2 x), itself and 2^(E - PB) normal numbers
-                    const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, PB - 126), 126);
+                    // 2^-floor(log2 x), itself and 2^E normal numbers
+                    const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, -126), 126);
                     const float c = exp2i(-e);
                     if (cb[j] == 0.0f || c < cb[j]) {
                         const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
@@ -768,7 +769,8 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                     for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
             }
         }
-        const float b0 = m0 == -INFINITY ? 0.0f : m0, b1 = m1 == -INFINITY ? 0.0f : m1;
+        // weights and their sums times 2^PB
+        const float b0 = m0 == -INFINITY ? 0.0f : m0 - PB, b1 = m1 == -INFINITY ? 0.0f : m1 - PB;
         s[0] = ex2(s[0] - b0);
         s[1] = ex2(s[1] - b1);
         s[2] = ex2(s[2] - b0);
@@ -794,34 +796,44 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                 at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, vs[i]);
             }
         }
-        // weights p of the lane's tokens and column head, times 2^PB
-        float pw[NTH][4];
+        // weights of the lane's tokens and column: head g >> 1 (+ 4 q), parity g & 1
+        float pw[NTH][4];                     // (VM 0, or two pieces)
+        uint32_t wv[NTH][PC][4];              // (VM 1, 2) as f16 pieces, (w, 0) or (0, w)
+        const bool odd = (g >> 1) & 1;
+        const uint32_t par = (g & 1) ? 0x3c000000u : 0x00003c00u;
+        if constexpr (VM && !HP) {
+            const __half2 h0 = __floats2half2_rn(s[0], s[1]), h1 = __floats2half2_rn(s[2], s[3]);
+            const uint32_t k0 = *reinterpret_cast<const uint32_t *>(&h0), k1 = *reinterpret_cast<const uint32_t *>(&h1);
+            const uint32_t pick = (g & 1) ? (odd ? 0x3244u : 0x1044u) : odd ? 0x4432u : 0x4410u;
 #pragma unroll
-        for (int q = 0; q < NTH; ++q) {
-            const int src = (g >> 2) + 2 * q;       // lane part of head (g >> 1) + 4 q
-            const bool odd = (g >> 1) & 1;
+            for (int q = 0; q < NTH; ++q)
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x0 = __shfl_sync(0xffffffffu, s[0], (t + 4 * i) * 4 + src), x1 = __shfl_sync(0xffffffffu, s[1], (t + 4 * i) * 4 + src);
-                const float y0 = __shfl_sync(0xffffffffu, s[2], (t + 4 * i) * 4 + src), y1 = __shfl_sync(0xffffffffu, s[3], (t + 4 * i) * 4 + src);
-                pw[q][i] = __fmul_rn(odd ? x1 : x0, (float)(1 << PB));
-                pw[q][2 + i] = __fmul_rn(odd ? y1 : y0, (float)(1 << PB));
-            }
-        }
-        const uint32_t par = (g & 1) ? 0x3c000000u : 0x00003c00u;   // the column's parity: (1, 0) or (0, 1)
-        uint32_t wv[NTH][PC][4];              // (VM 1, 2) the weights as f16 pieces
-        if constexpr (VM) {
+                for (int i = 0; i < 2; ++i) {
+                    const int from = (t + 4 * i) * 4 + (g >> 2) + 2 * q;
+                    wv[q][0][i] = __byte_perm(__shfl_sync(0xffffffffu, k0, from), 0u, pick);
+                    wv[q][0][2 + i] = __byte_perm(__shfl_sync(0xffffffffu, k1, from), 0u, pick);
+                }
+        } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int q = 0; q < NTH; ++q) {
 #pragma unroll
-                for (int q = 0; q < NTH; ++q) {
-                    const uint32_t h = half2_of(pw[q][i]);
-                    wv[q][0][i] = hmul2_u(h, par);
-                    if (HP) {
+                for (int i = 0; i < 2; ++i) {
+                    const int from = (t + 4 * i) * 4 + (g >> 2) + 2 * q;
+                    const float x0 = __shfl_sync(0xffffffffu, s[0], from), x1 = __shfl_sync(0xffffffffu, s[1], from);
+                    const float y0 = __shfl_sync(0xffffffffu, s[2], from), y1 = __shfl_sync(0xffffffffu, s[3], from);
+                    pw[q][i] = odd ? x1 : x0;
+                    pw[q][2 + i] = odd ? y1 : y0;
+                }
+                if constexpr (VM) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t h = half2_of(pw[q][i]);
                         const float back = __low2float(*reinterpret_cast<const __half2 *>(&h));
+                        wv[q][0][i] = hmul2_u(h, par);
                         wv[q][PC - 1][i] = hmul2_u(half2_of(__fmul_rn(__fsub_rn(pw[q][i], back), 2048.0f)), par);
                     }
                 }
+            }
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
@@ -918,16 +930,16 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         const bool whole = p.splits == 1;
         // over the sum (a stretch's too, whose sum of large values might pass
         // binary32); of no tokens: zeros
-        const float div = l > 0.0f || l != l ? __fdiv_rn(1.0f, l) : 0.0f;
+        const float div = at_over(l);
         if (g == 0) {
-            if (p.joined) *reinterpret_cast<float2 *>(mine + 4 * NTH * D + 2 * head) = make_float2(m, l);
-            else if (!whole) p.part_ml[out * p.splits + split] = make_float2(m, l);
-            else if (p.lse) p.lse[out] = l > 0.0f || l != l ? (m + log2f(l)) * 0.693147180559945309417f : -INFINITY;
+            if (p.joined) *reinterpret_cast<float2 *>(mine + 4 * NTH * D + 2 * head) = make_float2(m - PB, l);
+            else if (!whole) p.part_ml[out * p.splits + split] = make_float2(m - PB, l);
+            else if (p.lse) p.lse[out] = l > 0.0f || l != l ? (m - PB + log2f(l)) * 0.693147180559945309417f : -INFINITY;
         }
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
-            // 2^(E - PB) of the block, the tensor scale, the sum
-            const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - PB - (int)(__float_as_uint(cb[j]) >> 23)), vts);
+            // 2^E of the block, the tensor scale
+            const float f = cb[j] == 0.0f ? 0.0f : __fmul_rn(exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)), vts);
             float o[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] = div == 0.0f ? 0.0f : __fmul_rn(__fmul_rn(acc[q][j][i], div), f);
@@ -971,9 +983,16 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
 #pragma unroll 4
         for (int s = sub; s < p.splits; s += step) {
             const float *r = reinterpret_cast<const float *>(smem_at + s * G::WARP);
-            const float w = at_weight(*reinterpret_cast<const float2 *>(r + 4 * NTH * D + 2 * head), m);
+            l += at_weight(*reinterpret_cast<const float2 *>(r + 4 * NTH * D + 2 * head), m);
+        }
+        __syncwarp();
+        for (int x = 1; x < step; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const float inv = at_over(l);         // (weights of 1 at most: no sum passes binary32)
+#pragma unroll 4
+        for (int s = sub; s < p.splits; s += step) {
+            const float *r = reinterpret_cast<const float *>(smem_at + s * G::WARP);
+            const float w = __fmul_rn(at_weight(*reinterpret_cast<const float2 *>(r + 4 * NTH * D + 2 * head), m), inv);
             const float4 v = *reinterpret_cast<const float4 *>(r + head * D + d);
-            l += w;
             o[0] = fmaf(w, v.x, o[0]);
             o[1] = fmaf(w, v.y, o[1]);
             o[2] = fmaf(w, v.z, o[2]);
@@ -981,7 +1000,6 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         }
         __syncwarp();
         for (int x = 1; x < step; x <<= 1) {
-            l += __shfl_xor_sync(0xffffffffu, l, x);
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[i] += __shfl_xor_sync(0xffffffffu, o[i], x);
         }
