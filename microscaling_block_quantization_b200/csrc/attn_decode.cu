@@ -83,8 +83,8 @@ AtPick at_pick(int el, int d, int bs, int nth, int hp, int sfmt)
 
 }  // namespace
 
-// How a call of these sizes is split (times on a B200, 32 query and 8 key heads
-// of 128, MXFP4 unless said).  As many stretches of 32 tokens at least as run at
+// How a call of these sizes is split (times on a B200, both sides measured with one
+// kernel, a tenth slower than now; 32 query and 8 key heads of 128, MXFP4 unless said).  As many stretches of 32 tokens at least as run at
 // once (`warps_sm` warps of the kernel an SM); where several long sequences give
 // stretches of 256 tokens and more, twice as many, so that a warp that is done
 // makes room for another: 64 sequences of up to 8192 tokens 176 -> 156 us, but

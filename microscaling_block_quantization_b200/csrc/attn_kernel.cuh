@@ -26,12 +26,13 @@
 //   eight columns (head, parity), and the weight of column (h, r) at (t, e) is
 //   p_t(h) where e = r, else 0: code pairs enter the instruction as decoded,
 //   nothing is transposed, and each m16 tile is one 32-block of the head, so
-//   that the block's scale multiplies the weight: w = p s_b, in binary32.
+//   that the block's scale multiplies the weight: w = p s_b, in binary32 (E8M0
+//   scales and bf16 results, VM = 2: in f16, by a power of two).
 // * E4M3 scales with E2M1 codes (NVFP4; VM = 1) need no such folding: the
 //   product of code and scale is an f16 exactly, so the codes are scaled as
 //   they are decoded, on the FMA pipe, and w is p alone.
 // * A tile's scale bytes are decoded once, a share a lane, and read back by all
-//   as words (64 x 8192 157 -> 138 us, 1 x 131072 NVFP4 67 -> 58 us).
+//   as words (157 -> 138 us below, NVFP4 67 -> 58 us).
 // * w as f16: scaled by 2^7 and, per 32-block, by a reference exponent of the
 //   block scales that also moves rarely, so w stays in [0, 2^15]; a weight is
 //   flushed only below 2^-32 of its block's largest.  One f16 rounding
@@ -42,9 +43,10 @@
 //   shared memory at the end of the kernel, else in a second launch.
 //
 // Measured (32 query heads, 8 key heads of 128): 64 sequences of up to 8192
-// tokens in MXFP4 138 us (3.1 TB/s), one of 131072 in NVFP4 58 us: bound by the
-// instructions that turn codes into operands and place the rows.  One sequence
-// of 1000 tokens 8.8 us: two launches, and 0.6 us for each 16 tokens of a warp.
+// tokens in MXFP4 132 us (3.3 TB/s), one of 131072 in NVFP4 57 us: the integer
+// and conversion pipe is 55% and the issue slots 61% taken (360 instructions for
+// 16 tokens of a key head).  One sequence of 1000 tokens 8.7 us: two launches,
+// and 0.6 us for each 16 tokens of a warp.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -144,6 +144,16 @@ def test_split_sequences(mx, name, seqs, n):
     run(mx, make(mx, configs(mx)[name], lengths, 8, 2, 128, 64, torch.float32, qgain=2.0))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("name,D", [("e2m3", 256), ("e3m2", 128), ("mxfp4", 256), ("int4", 64), ("nvfp4", 256)])
+def test_many_sequences_joined_in_a_cta(mx, name, D, dtype):
+    """A CTA's warps share a sequence, as many as their rings leave room for; fewer tiles than warps too."""
+    for seqs, n in ((40, 900), (40, 20), (90, 250)):
+        args = make(mx, configs(mx)[name], [n] * (seqs - 2) + [0, 7], 12, 2, D, 32, dtype)
+        run(mx, args)
+        run(mx, args[:3] + (args[3].clamp(max=33),))
+
+
 @pytest.mark.parametrize("Hq,H,name", [(4, 1, "mxfp4"), (14, 2, "nvfp4"), (9, 1, "e2m3")])
 def test_ragged_batches(mx, Hq, H, name):
     """Long, short and empty sequences of one batch; batches shorter than the table allows."""
