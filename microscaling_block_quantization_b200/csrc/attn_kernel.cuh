@@ -34,10 +34,20 @@
 // * A tile's scale bytes are decoded once, a share a lane, and read back by all
 //   as words (157 -> 138 us below, NVFP4 67 -> 58 us).
 // * w as f16: scaled by 2^7 and, per 32-block, by a reference exponent of the
-//   block scales that also moves rarely, so w stays in [0, 2^15]; a weight is
-//   flushed only below 2^-32 of its block's largest.  One f16 rounding
-//   (2^-11) per weight for bf16 results; for binary32 a second piece holds
-//   the rounding's remainder (2^-22).
+//   block scales that also moves rarely, so w stays in [0, 2^15] and is dropped
+//   below 2^-25, which is p s_b below 2^-32 of the reference.  One f16 rounding
+//   (2^-12 of the weight) for bf16 results; for binary32 a second piece holds
+//   the rounding's remainder (2^-23).
+// * A stretch in which a block's scale (but code 0) has been below 2^-6 of the
+//   reference, or has moved it up, could lose its largest products that way: a
+//   token of weight 1 and a value 2^-26 of another's.  From that tile on the
+//   products p v are formed with w as TF32, the same 11 bits (binary32: two
+//   pieces) with binary32's exponents, four m16n8k8 instructions for two, and
+//   nothing is dropped, in a loop of its own: as a branch of the one loop it cost
+//   every call 5% (64 x 8192 134 -> 140 us, this way 136).  So w is dropped only
+//   below 2^-24 of the largest weight times the block's smallest scale (2^-26 but at
+//   the top of UE5M3).  VM = 1, whose weights are p alone, drops p below 2^-35 of
+//   the largest.
 // * Partial results (each stretch's own attention, m, l) of a sequence's
 //   stretches meet in a fixed order: where a CTA's warps hold them all, in
 //   shared memory at the end of the kernel, else in a second launch.
@@ -51,6 +61,8 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mma_decode.cuh"
 #include "mx_internal.h"
@@ -299,6 +311,18 @@ __device__ __forceinline__ void at_load8(const AttnParams &p, int64_t at, bool o
             for (int i = 0; i < 8; ++i) v[i] = bits2f((uint32_t)x[i] << 16);
         }
     }
+}
+
+// The scale of 32-block j (blocks of 16: its half u) of a tile's value token, by
+// itself.  shift: bits to the token's first scale in its word.
+template <int EL, int D, int BS>
+__device__ __forceinline__ float at_value_scale(const AttnParams &p, uint32_t st, int tok, uint32_t shift, int j, int u)
+{
+    using G = AtGeom<EL, D, BS>;
+    const uint32_t at = BS == 16 ? 2 * j + u : G::NARROW ? (shift >> 3) + ((32 * j) >> p.log2B) : j;
+    uint32_t b;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(b) : "r"(st + G::VS_AT + tok * G::SW + at));
+    return scale1(p.sfmt, b);
 }
 
 // visible tokens of a sequence, and the token of visible index i
@@ -594,93 +618,18 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
     }
 
     const uint32_t k_lane = at_key_lane<EL, D, BS>(g, t), v_lane = at_value_lane<EL, D, BS>(g, t), v_sel = at_value_sel<BS>(g);
-    uint32_t lim[(G::SW + 7) / 8] = {};       // limits of the lane's share of value scale bytes
+    uint32_t lim[(G::SW + 7) / 8] = {};       // upper limits of the lane's share of value scale bytes
+    const uint32_t span = p.sfmt == S_E8M0 ? 9u : 72u;   // codes from 2^-6 to 2^3 (an exponent is 8 codes of a minifloat)
+    bool wide = false;                        // value scales too far apart for f16 weights
     float cl[(G::SW + 7) / 8 * 4] = {};       // and their blocks' 2^-E
     const uint32_t words = ring + G::SCALES_AT;
     uint32_t st = ring;
-    for (int tile = tile0; tile < tile1; ++tile) {
-        cp_async_wait<G::STAGES - 2>();
-        __syncwarp();                         // the tile is in, and the last one is read
-        issue();
-        uint4 meta;
-        if (G::NARROW) meta = lds128(st + G::META_AT);
-        else meta = make_uint4(lds32(st + G::META_AT), 0u, 0u, 0u);
-        // where a token's scales begin in their word
-        const auto shift_of = [&](int tk) { return G::NARROW ? (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8 : 0u; };
-
-        if constexpr (VM != 1) {
-            // A value scale past 2^3 times its block's reference, or no reference
-            // yet?  The codes of scales order like their values, so each lane
-            // compares its share of the tile's scale bytes with the limits' codes.
-            bool past = false;
-            if (G::NARROW) {
-                past = cb[0] == 0.0f;
-    #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float x[NB * SUB];
-                    at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, cb, x);
-    #pragma unroll
-                    for (int j = 0; j < NB * SUB; ++j) past |= x[j] > 8.0f;
-                }
-            } else {
-                const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
-    #pragma unroll
-                for (int i = 0; i < (G::SW + 7) / 8; ++i) {
-                    const uint32_t w = G::SW == 4 ? lds16(a) : lds32(a + 4 * i);
-    #pragma unroll
-                    for (int k = 0; k < (G::SW == 4 ? 2 : 4); ++k) past |= ((w >> (8 * k)) & 0xffu) > ((lim[i] >> (8 * k)) & 0xffu);
-                }
-            }
-            if (__any_sync(0xffffffffu, past)) {
-                float x[NB], one[NB];
-    #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    x[j] = 0.0f;
-                    one[j] = 1.0f;
-                }
-    #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y[NB * SUB];
-                    at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, one, y);
-    #pragma unroll
-                    for (int j = 0; j < NB * SUB; ++j) x[j / SUB] = fmaxf(x[j / SUB], y[j]);
-                }
-    #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
-                    x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
-                    // 2^-floor(log2 x), itself and 2^E normal numbers
-                    const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, -126), 126);
-                    const float c = exp2i(-e);
-                    if (cb[j] == 0.0f || c < cb[j]) {
-                        const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
-    #pragma unroll
-                        for (int q = 0; q < NTH; ++q)
-    #pragma unroll
-                            for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
-                        cb[j] = c;
-                    }
-                }
-                if (!G::NARROW) {
-                    // the limits of the lane's bytes: the code of 2^(E + 3)
-    #pragma unroll
-                    for (int i = 0; i < (G::SW + 7) / 8; ++i) {
-                        lim[i] = 0u;
-    #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const int at = (lane * (G::SW / 2) + 4 * i + k) & (G::SW - 1);   // the byte's scale
-                            int e = 0;
-    #pragma unroll
-                            for (int j = 0; j < NB; ++j)
-                                if (at / SUB == j) e = 127 - (int)(__float_as_uint(cb[j]) >> 23);
-                            const int code = p.sfmt == S_E8M0 ? e + 130 : (e + 3 + (p.sfmt == S_UE4M3 ? 7 : 15)) * 8;
-                            lim[i] |= (uint32_t)min(max(code, 0), 255) << (8 * k);
-                            cl[4 * i + k] = exp2i(-e);
-                        }
-                    }
-                }
-            }
-        }
+    uint4 meta;                               // tokens that are there, and
+    // where a token's scales begin in their word
+    const auto shift_of = [&](int tk) { return G::NARROW ? (((meta.y >> tk) & 1) | (((meta.z >> tk) & 1) << 1)) * 8 : 0u; };
+    // A tile's scores, weights and products, and on to the next.
+    const auto tile_sums = [&](auto wide_tag) {
+        constexpr bool WIDE = decltype(wide_tag)::value;
         // the tile's scales, each decoded by one lane
         if constexpr (!G::NARROW) {
             at_spread_scales<G::SW, AS_F32>(p.sfmt, st + G::KS_AT, words, lane, nullptr);
@@ -779,6 +728,58 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
         s[3] = ex2(s[3] - b1);
         l0 += s[0] + s[2];
         l1 += s[1] + s[3];
+
+        if constexpr (WIDE) {
+            // Token t + 4 i of parity e is k = t (+ 4) of the instruction for that
+            // parity: the columns of the other parity have weight zero.
+#pragma unroll
+            for (int q = 0; q < NTH; ++q) {
+                float w[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int from = (t + 4 * (i & 1)) * 4 + (g >> 2) + 2 * q;
+                    const float x0 = __shfl_sync(0xffffffffu, s[i & 2], from), x1 = __shfl_sync(0xffffffffu, s[(i & 2) + 1], from);
+                    w[i] = (g >> 1) & 1 ? x1 : x0;
+                }
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    uint32_t lo[4], hi[4];
+                    at_value_codes<EL, D, BS, 0>(st + v_lane, j, v_sel, lo, hi);
+                    at_value_codes<EL, D, BS, 2>(st + v_lane, j, v_sel, lo + 2, hi + 2);
+#pragma unroll
+                    for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+                        for (int i = 0; i < 4; i += 2) {
+                            float x[2];
+#pragma unroll
+                            for (int k = 0; k < 2; ++k) {
+                                const int tk = t + 4 * (i + k);
+                                x[k] = __fmul_rn(w[i + k], __fmul_rn(at_value_scale<EL, D, BS>(p, st, tk, shift_of(tk), j, u), cb[j]));
+                            }
+#pragma unroll
+                            for (int piece = 0; piece < PC; ++piece) {
+                                uint32_t b[2];
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) {
+                                    b[k] = tf32_of(x[k]);
+                                    x[k] = __fsub_rn(x[k], bits2f(b[k]));
+                                }
+#pragma unroll
+                                for (int e = 0; e < 2; ++e) {
+                                    const uint32_t b0 = (g & 1) == e ? b[0] : 0u, b1 = (g & 1) == e ? b[1] : 0u;
+                                    // (blocks of 16: the rows of the half's own pairs)
+                                    const bool l = SUB == 1 || u == 0, h = SUB == 1 || u == 1;
+                                    mma_1688_tf32(acc[q][j], l ? tf32_of_half(lo[i], e) : 0u, h ? tf32_of_half(hi[i], e) : 0u,
+                                                  l ? tf32_of_half(lo[i + 1], e) : 0u, h ? tf32_of_half(hi[i + 1], e) : 0u, b0, b1);
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            st = st + G::STAGE == ring + G::STAGES * G::STAGE ? ring : st + G::STAGE;
+            return;
+        }
 
         float vs[4][NB * SUB];                // (VM 0) value scales of tokens t, t + 4, t + 8, t + 12 over the references
         uint32_t vh[4][NB * SUB];             // (else) as f16 pairs: the scales, or over the references
@@ -907,6 +908,115 @@ __global__ void __launch_bounds__(32 * at_warps<D, BS, NTH, HP>(), 1) k_attn(con
                 }
         }
         st = st + G::STAGE == ring + G::STAGES * G::STAGE ? ring : st + G::STAGE;
+    };
+    // Is a value scale of the tile past 2^3 times its block's reference, or below
+    // 2^-6 of it?  Code 0 is not: a block of zeros, or a token that is not there
+    // (2^-127 beside larger scales counts as zero).  Each lane looks at its share of
+    // the tile's scales; their codes order like their values.
+    const auto outside = [&]() {
+        bool past = false;
+        if (G::NARROW) {
+            // (a token a lane, its even or odd 32-blocks)
+#pragma unroll
+            for (int j = 0; j < NB; j += 2) {
+                const float y = at_value_scale<EL, D, BS>(p, st, lane & 15, shift_of(lane & 15), j + (lane >> 4), 0);
+                const float x = __fmul_rn(y, lane < 16 ? cb[j] : cb[j + 1]);
+                past |= x > 8.0f || (x < 0x1p-6f && y > 0x1p-127f);
+            }
+        } else {
+            const uint32_t a = st + G::VS_AT + lane * (G::SW / 2);
+#pragma unroll
+            for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                const uint32_t w = G::SW == 4 ? lds16(a) : lds32(a + 4 * i);
+#pragma unroll
+                for (int k = 0; k < (G::SW == 4 ? 2 : 4); ++k) {
+                    const uint32_t c = (w >> (8 * k)) & 0xffu;
+                    past |= ((lim[i] >> (8 * k)) & 0xffu) - c > span && c;
+                }
+            }
+        }
+        return past;
+    };
+    // New references where the tile's value scales ask for them; and are they too far
+    // apart for f16 weights from here on?
+    const auto references = [&]() {
+        float x[NB], one[NB];
+        bool far = false;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            x[j] = 0.0f;
+            one[j] = 1.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float y[NB * SUB];
+            at_scales<EL, D, BS>(p, st + G::VS_AT, t + 4 * i, shift_of(t + 4 * i), sel, one, y);
+#pragma unroll
+            for (int j = 0; j < NB * SUB; ++j) x[j / SUB] = fmaxf(x[j / SUB], y[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+            x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 1));
+            x[j] = fmaxf(x[j], __shfl_xor_sync(0xffffffffu, x[j], 2));
+            // 2^-floor(log2 x), itself and 2^E normal numbers
+            const int e = min(max((int)(__float_as_uint(x[j]) >> 23) - 127, -126), 126);
+            const float c = exp2i(-e);
+            if (cb[j] == 0.0f || 8.0f * c <= cb[j]) {
+                far |= cb[j] != 0.0f;
+                const float r = cb[j] == 0.0f ? 1.0f : __fmul_rn(c, exp2i(127 - (int)(__float_as_uint(cb[j]) >> 23)));
+#pragma unroll
+                for (int q = 0; q < NTH; ++q)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) acc[q][j][i] *= r;
+                cb[j] = c;
+            }
+        }
+        if (!G::NARROW) {
+            // the limits of the lane's bytes: the code of 2^(E + 3)
+#pragma unroll
+            for (int i = 0; i < (G::SW + 7) / 8; ++i) {
+                lim[i] = 0u;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const int at = (lane * (G::SW / 2) + 4 * i + k) & (G::SW - 1);   // the byte's scale
+                    int e = 0;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j)
+                        if (at / SUB == j) e = 127 - (int)(__float_as_uint(cb[j]) >> 23);
+                    const int code = p.sfmt == S_E8M0 ? e + 130 : (e + 3 + (p.sfmt == S_UE4M3 ? 7 : 15)) * 8;
+                    lim[i] |= (uint32_t)min(max(code, 0), 255) << (8 * k);
+                    cl[4 * i + k] = exp2i(-e);
+                }
+            }
+        }
+        wide |= __any_sync(0xffffffffu, far || outside());
+    };
+    const auto arrive = [&]() {
+        cp_async_wait<G::STAGES - 2>();
+        __syncwarp();                         // the tile is in, and the last one is read
+        issue();
+        if (G::NARROW) meta = lds128(st + G::META_AT);
+        else meta = make_uint4(lds32(st + G::META_AT), 0u, 0u, 0u);
+    };
+    int tile = tile0;
+    for (; tile < tile1; ++tile) {
+        arrive();
+        if constexpr (VM != 1) {
+            if (__any_sync(0xffffffffu, outside() || tile == tile0)) {
+                references();
+                if (wide) break;
+            }
+        }
+        tile_sums(std::false_type());
+    }
+    if constexpr (VM != 1) {
+        // the rest of a stretch, whose tile is in
+        while (tile < tile1) {
+            tile_sums(std::true_type());
+            if (++tile == tile1) break;
+            arrive();
+            references();
+        }
     }
     cp_async_wait<0>();
 

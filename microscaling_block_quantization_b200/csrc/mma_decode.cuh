@@ -185,6 +185,26 @@ __device__ __forceinline__ void mma_1688_zero(float d[4], uint32_t a0, uint32_t 
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3]) : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
 }
 
+// D (16 x 8, binary32) += A (16 x 8, TF32) B (8 x 8, TF32): A rows g, g + 8 at
+// k = t (a0, a1) and t + 4 (a2, a3), B column g at the same k.
+__device__ __forceinline__ void mma_1688_tf32(float d[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1)
+{
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// binary32 rounded to TF32 (11 significant bits), and one half of an f16 pair as TF32 (exact)
+__device__ __forceinline__ uint32_t tf32_of(float x)
+{
+    uint32_t r;
+    asm("cvt.rna.tf32.f32 %0, %1;" : "=r"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t tf32_of_half(uint32_t pair, int high)
+{
+    const __half2 h = *reinterpret_cast<const __half2 *>(&pair);
+    return __float_as_uint(high ? __high2float(h) : __low2float(h));
+}
+
 // asynchronous global -> shared copies; bytes beyond src_bytes are zero
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int src_bytes)
 {
