@@ -18,6 +18,7 @@ import ctypes as C
 import dataclasses
 import importlib.util
 import os
+import threading
 
 import torch
 
@@ -69,8 +70,16 @@ class mx_sizes(C.Structure):
                 ("n_offsets", C.c_int64), ("workspace_bytes", C.c_int64), ("n_blocks", C.c_int64)]
 
 
+_struct_lock = threading.Lock()
+
+
+class _WithStruct:
+    """Room beside an instance's fields for its C struct."""
+    __slots__ = ("_struct",)
+
+
 @dataclasses.dataclass(frozen=True)
-class Config:
+class Config(_WithStruct):
     """One quantization configuration (fields of ``mx_config``)."""
     elem: int = E2M1
     scale_fmt: int = SCALE_E8M0
@@ -91,23 +100,25 @@ class Config:
                          self.axis, self.round, self.asymmetric, self.tensor_scale,
                          self.macro_block, self.hadamard, self.sf_layout, self.seed)
 
+    def _held(self):
+        """(struct, its reference, its address): made once, and kept in one
+        assignment that no other thread's replaces."""
+        try:
+            return self._struct
+        except AttributeError:
+            with _struct_lock:
+                if not hasattr(self, "_struct"):
+                    c = self.c()
+                    object.__setattr__(self, "_struct", (c, C.byref(c), C.addressof(c)))
+            return self._struct
+
     def ref(self):
-        """The C struct by reference, built once per instance."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            c = self.c()
-            r = C.byref(c)
-            object.__setattr__(self, "_ref", r)
-            object.__setattr__(self, "_address", C.addressof(c))    # (_ref keeps the struct)
-        return r
+        """The C struct by reference."""
+        return self._held()[1]
 
     def address(self) -> int:
         """Where the C struct is, for the compiled binding."""
-        a = self.__dict__.get("_address")
-        if a is None:
-            self.ref()
-            a = self._address
-        return a
+        return self._held()[2]
 
 
 MXFP4 = Config()
