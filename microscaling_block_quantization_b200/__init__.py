@@ -112,6 +112,10 @@ class Config(_WithStruct):
                     object.__setattr__(self, "_struct", (c, C.byref(c), C.addressof(c)))
             return self._struct
 
+    def __getstate__(self):
+        """The fields alone: a copy, or a configuration read back, makes its own struct."""
+        return dict(self.__dict__)
+
     def ref(self):
         """The C struct by reference."""
         return self._held()[1]
