@@ -589,7 +589,7 @@ class KVCache:
     """A paged cache of attention keys and values in a block-scaled format:
     ``pages * page_size`` rows of ``kv_heads * head_dim`` elements, ``k`` and ``v`` as
     ``quantize`` would hold such a tensor (``dequantize(cache.k)`` reads it back).
-    The buffers must stay those the cache was made with."""
+    Every call looks at the fields anew, and refuses buffers too small for them."""
     cfg: Config
     pages: int
     page_size: int
@@ -598,33 +598,26 @@ class KVCache:
     k: Quantized
     v: Quantized
 
-    def ref(self):
-        """The C struct by reference, built once per cache."""
-        r = self.__dict__.get("_ref")
-        if r is None:
-            rows, cols, bits = self.pages * self.page_size, self.kv_heads * self.head_dim, 8 if self.cfg.elem in FP6 else 4
-            for name, t in (("k", self.k), ("v", self.v)):
-                if any(u is not None and u.device != self.device for u in (t.codes, t.scales, t.tensor_scale if self.cfg.tensor_scale else None)):
-                    raise ValueError(f"{name}: every buffer must be on {self.device}")
-                if (t.codes.numel() * t.codes.element_size() < rows * cols * bits // 8 or not t.codes.is_contiguous() or
-                        t.scales.numel() < rows * (cols // self.cfg.block) or not t.scales.is_contiguous()):
-                    raise ValueError(f"{name}: buffers too small for {rows} rows of {cols}, or not contiguous")
-                if self.cfg.tensor_scale and (t.tensor_scale is None or t.tensor_scale.dtype != torch.float32):
-                    raise TypeError(f"{name}: a float32 tensor scale is needed")
-            ts = [t.tensor_scale.data_ptr() if self.cfg.tensor_scale else None for t in (self.k, self.v)]
-            c = mx_kv_cache(self.k.codes.data_ptr(), self.v.codes.data_ptr(), self.k.scales.data_ptr(),
-                            self.v.scales.data_ptr(), ts[0], ts[1], self.pages, self.page_size, self.kv_heads, self.head_dim)
-            r = C.byref(c)
-            self.__dict__["_ref"], self.__dict__["_address"] = r, C.addressof(c)
-        return r
+    def _parts(self):
+        """What the compiled binding takes of a cache."""
+        cfg, k, v = self.cfg, self.k, self.v
+        return (cfg, cfg.address(), cfg.tensor_scale, k.codes, k.scales, k.tensor_scale, v.codes, v.scales, v.tensor_scale,
+                self.pages, self.page_size, self.kv_heads, self.head_dim)
 
-    def address(self) -> int:
-        """Where the C struct is, for the compiled binding."""
-        a = self.__dict__.get("_address")
-        if a is None:
-            self.ref()
-            a = self._address
-        return a
+    def ref(self):
+        """The C struct of the buffers as they are now, by reference."""
+        rows, cols, bits = self.pages * self.page_size, self.kv_heads * self.head_dim, 8 if self.cfg.elem in FP6 else 4
+        for name, t in (("k", self.k), ("v", self.v)):
+            if any(u is not None and u.device != self.device for u in (t.codes, t.scales, t.tensor_scale if self.cfg.tensor_scale else None)):
+                raise ValueError(f"{name}: every buffer must be on {self.device}")
+            if (t.codes.numel() * t.codes.element_size() < rows * cols * bits // 8 or not t.codes.is_contiguous() or
+                    t.scales.numel() < rows * (cols // self.cfg.block) or not t.scales.is_contiguous()):
+                raise ValueError(f"{name}: buffers too small for {rows} rows of {cols}, or not contiguous")
+            if self.cfg.tensor_scale and (t.tensor_scale is None or t.tensor_scale.dtype != torch.float32 or t.tensor_scale.numel() < 1):
+                raise TypeError(f"{name}: a float32 tensor scale is needed")
+        ts = [t.tensor_scale.data_ptr() if self.cfg.tensor_scale else None for t in (self.k, self.v)]
+        return C.byref(mx_kv_cache(self.k.codes.data_ptr(), self.v.codes.data_ptr(), self.k.scales.data_ptr(), self.v.scales.data_ptr(),
+                                   ts[0], ts[1], self.pages, self.page_size, self.kv_heads, self.head_dim))
 
     @property
     def device(self):
@@ -666,8 +659,7 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
         with torch.cuda.stream(stream):
             return kv_append(cache, q, k, v, slots, positions, q_gain=q_gain, k_gain=k_gain, eps=eps, inv_freq=inv_freq,
                              interleaved=interleaved, q_out=q_out, k_out=k_out)
-    r = _binding().kv_append(cache.cfg.address(), cache.address(), cache.k.codes, cache.head_dim, cache.kv_heads, q, k, v, slots,
-                             positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out)
+    r = _binding().kv_append(*cache._parts(), q, k, v, slots, positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out)
     if r.__class__ is int:
         _check("mx_kv_append", r)
     return r
@@ -688,9 +680,8 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengt
         with torch.cuda.stream(stream):
             return attn_decode(cache, q, page_table, lengths, scale=scale, window=window, sinks=sinks, lse=lse,
                                out_dtype=out_dtype, out=out, workspace=workspace)
-    D = cache.head_dim
-    r = _binding().attn_decode(cache.cfg.address(), cache.address(), cache.k.codes, D, q, page_table, lengths,
-                               D ** -0.5 if scale is None else scale, window, sinks, lse, out_dtype, out, workspace)
+    r = _binding().attn_decode(*cache._parts(), q, page_table, lengths, cache.head_dim ** -0.5 if scale is None else scale, window,
+                               sinks, lse, out_dtype, out, workspace)
     if r.__class__ is int:
         _check("mx_attn_decode", r)
     return r

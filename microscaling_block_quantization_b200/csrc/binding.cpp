@@ -128,6 +128,54 @@ void buffer(const at::Tensor *t, int64_t n, const char *name)
 }
 void *stream_of(c10::Device d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 
+// A cache as a call finds it: its tensors are looked at every time, so that none
+// that was replaced is written to.
+struct Cache {
+    mx_kv_cache c;
+    const at::Tensor *all[6];
+    int64_t heads, dim;
+};
+constexpr int kCacheArgs = 13;
+// cfg (held by the caller's arguments), cfg address, uses tensor scales, codes, scales and tensor scale of keys, of values, pages,
+// page_size, kv_heads, head_dim
+const mx_config *cache_of(PyObject *const *a, Cache &r)
+{
+    const mx_config *cfg = address<mx_config>(a[1]);
+    const bool ts = PyObject_IsTrue(a[2]);
+    const int64_t pages = integer(a[9], "pages"), page_size = integer(a[10], "page_size");
+    r.heads = integer(a[11], "kv_heads");
+    r.dim = integer(a[12], "head_dim");
+    if (page_size > INT32_MAX || r.heads > INT32_MAX || r.dim > INT32_MAX || page_size < INT32_MIN || r.heads < INT32_MIN || r.dim < INT32_MIN)
+        value_error("page_size, kv_heads and head_dim must fit 32 bits");
+    for (int h = 0; h < 2; ++h) {
+        const char *name = h ? "v" : "k";
+        const at::Tensor &codes = tensor(a[3 + 3 * h], "codes"), &scales = tensor(a[4 + 3 * h], "scales");
+        const at::Tensor *t = ts ? maybe(a[5 + 3 * h], "tensor_scale") : nullptr;
+        // (sizes that the library refuses are left to it)
+        if (pages >= 0 && page_size > 0 && pages <= INT32_MAX / page_size && r.heads > 0 && r.heads <= 4096 && r.dim > 0 && r.dim <= 256 &&
+            cfg->block > 0) {
+            const int64_t rows = pages * page_size, cols = r.heads * r.dim;
+            const int bits = cfg->elem == MX_E2M3 || cfg->elem == MX_E3M2 ? 8 : 4;
+            if ((int64_t)codes.nbytes() < rows * cols * bits / 8 || !codes.is_contiguous() ||
+                (int64_t)scales.nbytes() < rows * (cols / cfg->block) || !scales.is_contiguous())
+                value_error(std::string(name) + ": buffers too small for " + std::to_string(rows) + " rows of " + std::to_string(cols) +
+                            ", or not contiguous");
+        }
+        if (ts && (!t || t->scalar_type() != at::kFloat || t->numel() < 1)) type_error(std::string(name) + ": a float32 tensor scale is needed");
+        r.all[3 * h] = &codes;
+        r.all[3 * h + 1] = &scales;
+        r.all[3 * h + 2] = t;
+    }
+    r.c = {r.all[0]->data_ptr(), r.all[3]->data_ptr(), static_cast<uint8_t *>(r.all[1]->data_ptr()), static_cast<uint8_t *>(r.all[4]->data_ptr()),
+           static_cast<const float *>(ptr(r.all[2])), static_cast<const float *>(ptr(r.all[5])), pages, (int32_t)page_size, (int32_t)r.heads,
+           (int32_t)r.dim};
+    return cfg;
+}
+void cache_on(const Cache &r, c10::Device dev)
+{
+    for (const at::Tensor *t : r.all) same_device(t, dev, "the cache");
+}
+
 // x, codes, scales, tensor_scale, macro, offsets, cfg address, uses tensor scale, N, K, out_dtype, out
 PyObject *gemv(PyObject *const *a)
 {
@@ -176,26 +224,26 @@ PyObject *gemv(PyObject *const *a)
     return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(y));
 }
 
-// cfg, cache addresses, cache tensor, head_dim, kv_heads, q, k, v, slots, positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out
+// the cache (kCacheArgs), q, k, v, slots, positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out
 PyObject *kv_append(PyObject *const *a)
 {
-    const mx_config *cfg = address<mx_config>(a[0]);
-    const mx_kv_cache *cache = address<mx_kv_cache>(a[1]);
-    const at::Tensor &held = tensor(a[2], "the cache");
-    const int64_t D = integer(a[3], "head_dim"), H = integer(a[4], "kv_heads");
-    const at::Tensor *q = maybe(a[5], "q"), &k = on_cuda(a[6], "k"), &v = tensor(a[7], "v");
-    const at::Tensor &slots = tensor(a[8], "slots"), *positions = maybe(a[9], "positions");
-    const at::Tensor *q_gain = maybe(a[10], "q_gain"), *k_gain = maybe(a[11], "k_gain"), *freq = maybe(a[13], "inv_freq");
-    const at::Tensor *q_out = maybe(a[15], "q_out");
-    const bool make_k = a[16] == Py_True, no_k = a[16] == Py_False || a[16] == Py_None;
-    const at::Tensor *k_out = make_k || no_k ? nullptr : &tensor(a[16], "k_out");
+    Cache cache;
+    const mx_config *cfg = cache_of(a, cache);
+    const int64_t D = cache.dim, H = cache.heads;
+    a += kCacheArgs;
+    const at::Tensor *q = maybe(a[0], "q"), &k = on_cuda(a[1], "k"), &v = tensor(a[2], "v");
+    const at::Tensor &slots = tensor(a[3], "slots"), *positions = maybe(a[4], "positions");
+    const at::Tensor *q_gain = maybe(a[5], "q_gain"), *k_gain = maybe(a[6], "k_gain"), *freq = maybe(a[8], "inv_freq");
+    const at::Tensor *q_out = maybe(a[10], "q_out");
+    const bool make_k = a[11] == Py_True, no_k = a[11] == Py_False || a[11] == Py_None;
+    const at::Tensor *k_out = make_k || no_k ? nullptr : &tensor(a[11], "k_out");
     const c10::Device dev = k.device();
     const at::ScalarType s = k.scalar_type();
     const int32_t dt = dtype_code(s, "k");
     if (k.dim() < 1) value_error("k must have two or three dimensions");
     const int64_t T = k.size(0), ldk = heads_of(k, H, D, "k");
     const struct { const at::Tensor *t; const char *name; } like[] = {{&v, "v"}, {q, "q"}, {q_out, "q_out"}, {k_out, "k_out"}};
-    same_device(&held, dev, "the cache");
+    cache_on(cache, dev);
     for (const auto &l : like) {
         same_device(l.t, dev, l.name);
         if (l.t && (l.t->scalar_type() != s || l.t->dim() < 1 || l.t->size(0) != T))
@@ -207,7 +255,7 @@ PyObject *kv_append(PyObject *const *a)
     void *ps = vector(positions, T, at::kLong, dev, "positions"), *pf = vector(freq, rot / 2, at::kFloat, dev, "inv_freq");
     void *pq = vector(q_gain, D, at::kFloat, dev, "q_gain"), *pk = vector(k_gain, D, at::kFloat, dev, "k_gain");
     void *pl = vector(&slots, T, at::kLong, dev, "slots");
-    const float eps = real(a[12], "eps");
+    const float eps = real(a[7], "eps");
     const c10::cuda::CUDAGuard guard(dev);
     int64_t ldqo = Hq * D, ldko = H * D;
     at::Tensor qo, ko;
@@ -223,9 +271,9 @@ PyObject *kv_append(PyObject *const *a)
     } else if (make_k) {
         ko = at::empty({T, H, D}, k.options());
     }
-    const int rc = mx_kv_append(cfg, cache, ptr(q), k.data_ptr(), v.data_ptr(), dt, ldq, ldk, ldv, T, (int32_t)Hq,
+    const int rc = mx_kv_append(cfg, &cache.c, ptr(q), k.data_ptr(), v.data_ptr(), dt, ldq, ldk, ldv, T, (int32_t)Hq,
                                 static_cast<float *>(pq), static_cast<float *>(pk), eps, static_cast<float *>(pf), (int32_t)rot,
-                                PyObject_IsTrue(a[14]) ? 1 : 0, static_cast<int64_t *>(ps), static_cast<int64_t *>(pl),
+                                PyObject_IsTrue(a[9]) ? 1 : 0, static_cast<int64_t *>(ps), static_cast<int64_t *>(pl),
                                 qo.defined() ? qo.data_ptr() : nullptr, ldqo, ko.defined() ? ko.data_ptr() : nullptr, ldko, stream_of(dev));
     if (rc) return PyLong_FromLong(rc);
     PyObject *r = PyTuple_New(2);
@@ -239,22 +287,22 @@ PyObject *kv_append(PyObject *const *a)
     return r;
 }
 
-// cfg, cache addresses, cache tensor, head_dim, q, page_table, lengths, scale, window, sinks, lse, out_dtype, out, workspace
+// the cache (kCacheArgs), q, page_table, lengths, scale, window, sinks, lse, out_dtype, out, workspace
 PyObject *attn_decode(PyObject *const *a)
 {
-    const mx_config *cfg = address<mx_config>(a[0]);
-    const mx_kv_cache *cache = address<mx_kv_cache>(a[1]);
-    const at::Tensor &held = tensor(a[2], "the cache");
-    const int64_t D = integer(a[3], "head_dim");
-    const at::Tensor &q = on_cuda(a[4], "q"), &table = tensor(a[5], "page_table"), &lengths = tensor(a[6], "lengths");
-    const float scale = real(a[7], "scale");
-    const int64_t window = integer(a[8], "window"), sinks = integer(a[9], "sinks");
-    const bool want_lse = PyObject_IsTrue(a[10]);
-    const at::Tensor *out = maybe(a[12], "out"), *given = maybe(a[13], "workspace");
+    Cache cache;
+    const mx_config *cfg = cache_of(a, cache);
+    const int64_t D = cache.dim;
+    a += kCacheArgs;
+    const at::Tensor &q = on_cuda(a[0], "q"), &table = tensor(a[1], "page_table"), &lengths = tensor(a[2], "lengths");
+    const float scale = real(a[3], "scale");
+    const int64_t window = integer(a[4], "window"), sinks = integer(a[5], "sinks");
+    const bool want_lse = PyObject_IsTrue(a[6]);
+    const at::Tensor *out = maybe(a[8], "out"), *given = maybe(a[9], "workspace");
     const c10::Device dev = q.device();
     const int32_t qd = dtype_code(q.scalar_type(), "q");
     const int64_t Hq = head_count(q, D, "q"), S = q.size(0), ldq = heads_of(q, Hq, D, "q");
-    same_device(&held, dev, "the cache");
+    cache_on(cache, dev);
     same_device(&table, dev, "page_table");
     same_device(out, dev, "out");
     same_device(given, dev, "workspace");
@@ -267,17 +315,17 @@ PyObject *attn_decode(PyObject *const *a)
     if (given && (given->scalar_type() != at::kByte || !given->is_contiguous())) value_error("workspace must be contiguous uint8");
     if (window < INT32_MIN || window > INT32_MAX || sinks < INT32_MIN || sinks > INT32_MAX) value_error("window and sinks must fit 32 bits");
     if (out && (out->dim() < 1 || out->size(0) != S)) value_error("out must have " + std::to_string(S) + " rows");
-    const at::ScalarType os = wanted(a[11], out, q.scalar_type());
+    const at::ScalarType os = wanted(a[7], out, q.scalar_type());
     const int32_t od = dtype_code(os, "the result");
     const c10::cuda::CUDAGuard guard(dev);
     const int64_t ldo = out ? heads_of(*out, Hq, D, "out") : Hq * D;
     at::Tensor o = out ? *out : at::empty({S, Hq, D}, q.options().dtype(os));
     at::Tensor l, ws;
     if (want_lse) l = at::empty({S, Hq}, q.options().dtype(at::kFloat));
-    const int64_t nbytes = mx_attn_workspace_bytes(cache, S, (int32_t)Hq, pages, (int32_t)window, (int32_t)sinks);
+    const int64_t nbytes = mx_attn_workspace_bytes(&cache.c, S, (int32_t)Hq, pages, (int32_t)window, (int32_t)sinks);
     if (given) ws = *given;
     else if (nbytes) ws = at::empty({nbytes}, q.options().dtype(at::kByte));
-    const int rc = mx_attn_decode(cfg, cache, q.data_ptr(), qd, ldq, S, (int32_t)Hq, static_cast<int32_t *>(table.data_ptr()), ldt, pages,
+    const int rc = mx_attn_decode(cfg, &cache.c, q.data_ptr(), qd, ldq, S, (int32_t)Hq, static_cast<int32_t *>(table.data_ptr()), ldt, pages,
                                   static_cast<int32_t *>(pl), scale, (int32_t)window, (int32_t)sinks, o.data_ptr(), od, ldo,
                                   want_lse ? static_cast<float *>(l.data_ptr()) : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
                                   ws.defined() ? ws.numel() : 0, stream_of(dev));
@@ -328,7 +376,7 @@ template <PyObject *(*F)(PyObject *const *), int N> PyObject *call(PyObject *, P
 }
 
 #define MX_METHOD(f, n) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(&call<f, n>)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {MX_METHOD(gemv, 12), MX_METHOD(kv_append, 17), MX_METHOD(attn_decode, 14), MX_METHOD(dequantize, 9),
+PyMethodDef methods[] = {MX_METHOD(gemv, 12), MX_METHOD(kv_append, kCacheArgs + 12), MX_METHOD(attn_decode, kCacheArgs + 10), MX_METHOD(dequantize, 9),
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "mx_binding", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

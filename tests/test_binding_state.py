@@ -72,3 +72,75 @@ def test_used_configurations_are_copied_and_pickled(mx):
     file.seek(0)
     for other in (copy.deepcopy(q), pickle.loads(pickle.dumps(q)), torch.load(file, weights_only=False)):
         assert other.cfg == cfg and torch.equal(other.codes, q.codes) and other.codes.data_ptr() != q.codes.data_ptr()
+
+
+def given(mx):
+    return mx.Config(block=16, scale_fmt=mx.SCALE_UE4M3, rule=mx.RULE_NEAREST, tensor_scale=mx.TS_GIVEN)
+
+
+def small_cache(mx, cfg=None):
+    import torch
+    ts = dict(k_tensor_scale=torch.ones(1), v_tensor_scale=torch.ones(1)) if cfg and cfg.tensor_scale else {}
+    return mx.kv_cache(2, 4, 1, 64, cfg or mx.MXFP4, device="cpu", **ts)
+
+
+def pointers(c):
+    s = c.ref()._obj
+    return [s.k_codes, s.v_codes, s.k_scales, s.v_scales, s.k_tensor_scale, s.v_tensor_scale]
+
+
+def held(c):
+    return [t.data_ptr() for t in (c.k.codes, c.v.codes, c.k.scales, c.v.scales, c.k.tensor_scale, c.v.tensor_scale)]
+
+
+def test_a_used_cache_follows_its_tensors(mx):
+    """New buffers, tensor scales and sizes of a cache that was used are the ones of the next call."""
+    import copy
+    import pickle
+
+    import torch
+    c = small_cache(mx, given(mx))
+    assert pointers(c) == held(c)
+    c.k = copy.deepcopy(c.v)
+    c.v.codes = c.v.codes.clone()
+    c.v.tensor_scale = torch.ones(1)
+    assert pointers(c) == held(c)
+    for other in (copy.deepcopy(c), pickle.loads(pickle.dumps(c))):
+        assert pointers(other) == held(other) and not set(held(other)) & set(held(c))
+
+
+def calls(mx, c):
+    import torch
+    zeros = torch.zeros
+    return [lambda: mx.kv_append(c, None, zeros(1, 64), zeros(1, 64), zeros(1, dtype=torch.int64)),
+            lambda: mx.attn_decode(c, zeros(1, 1, 64), zeros(1, 2, dtype=torch.int32), zeros(1, dtype=torch.int32))]
+
+
+@pytest.mark.parametrize("change,error,text", [
+    (lambda c: setattr(c.k, "codes", c.k.codes[:100]), ValueError, "k: buffers too small"),
+    (lambda c: setattr(c.v, "codes", c.v.codes.repeat(2)[::2]), ValueError, "v: buffers too small"),
+    (lambda c: setattr(c.k, "scales", c.k.scales[:31]), ValueError, "k: buffers too small"),
+    (lambda c: setattr(c, "pages", 3), ValueError, "buffers too small"),
+    (lambda c: setattr(c, "head_dim", 128), ValueError, "buffers too small"),
+    (lambda c: setattr(c.v, "tensor_scale", None), TypeError, "v: a float32 tensor scale"),
+    (lambda c: setattr(c.k, "tensor_scale", c.k.tensor_scale.double()), TypeError, "k: a float32 tensor scale"),
+    (lambda c: setattr(c.k, "tensor_scale", c.k.tensor_scale[:0]), TypeError, "k: a float32 tensor scale"),
+])
+def test_a_changed_cache_is_checked_at_every_call(mx, change, error, text):
+    c = small_cache(mx, given(mx))
+    for call in calls(mx, c):
+        with pytest.raises(ValueError, match="CUDA"):        # all that is wrong before the change
+            call()
+    change(c)
+    for call in calls(mx, c) + [c.ref]:
+        with pytest.raises(error, match=text):
+            call()
+
+
+def test_a_cache_of_another_element_type_is_checked(mx):
+    c = small_cache(mx)
+    c.ref()
+    c.cfg = mx.Config(elem=mx.E2M3)                          # a byte a code
+    for call in calls(mx, c) + [c.ref]:
+        with pytest.raises(ValueError, match="buffers too small"):
+            call()
