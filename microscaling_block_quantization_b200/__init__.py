@@ -680,7 +680,7 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengt
         with torch.cuda.stream(stream):
             return attn_decode(cache, q, page_table, lengths, scale=scale, window=window, sinks=sinks, lse=lse,
                                out_dtype=out_dtype, out=out, workspace=workspace)
-    r = _binding().attn_decode(*cache._parts(), q, page_table, lengths, cache.head_dim ** -0.5 if scale is None else scale, window,
+    r = _binding().attn_decode(*cache._parts(), q, page_table, lengths, max(cache.head_dim, 1) ** -0.5 if scale is None else scale, window,
                                sinks, lse, out_dtype, out, workspace)
     if r.__class__ is int:
         _check("mx_attn_decode", r)

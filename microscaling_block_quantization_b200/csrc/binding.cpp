@@ -147,6 +147,7 @@ const mx_config *cache_of(PyObject *const *a, Cache &r)
     r.dim = integer(a[12], "head_dim");
     if (page_size > INT32_MAX || r.heads > INT32_MAX || r.dim > INT32_MAX || page_size < INT32_MIN || r.heads < INT32_MIN || r.dim < INT32_MIN)
         value_error("page_size, kv_heads and head_dim must fit 32 bits");
+    if (r.dim < 1) value_error("head_dim must be positive");   // (head counts are divided by it)
     for (int h = 0; h < 2; ++h) {
         const char *name = h ? "v" : "k";
         const at::Tensor &codes = tensor(a[3 + 3 * h], "codes"), &scales = tensor(a[4 + 3 * h], "scales");

@@ -144,3 +144,15 @@ def test_a_cache_of_another_element_type_is_checked(mx):
     for call in calls(mx, c) + [c.ref]:
         with pytest.raises(ValueError, match="buffers too small"):
             call()
+
+
+@pytest.mark.parametrize("dim", [0, -64])
+def test_a_cache_without_a_head_length_is_refused(mx, dim):
+    import torch
+    c = small_cache(mx)
+    c.head_dim = dim
+    q = torch.zeros(1, 0)
+    for call in calls(mx, c) + [lambda: mx.kv_append(c, q, q, q, torch.zeros(1, dtype=torch.int64)),
+                                lambda: mx.attn_decode(c, q, torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))]:
+        with pytest.raises(ValueError, match="head_dim"):
+            call()
