@@ -507,18 +507,40 @@ def new_workspace(cfg: Config, rows: int, cols: int, device) -> torch.Tensor:
     return torch.zeros(query_sizes(cfg, rows, cols).workspace_bytes, dtype=torch.uint8, device=device)
 
 
+def _check_held(q: Quantized) -> None:
+    """A ``Quantized``'s buffers, as the compiled binding checks them."""
+    s = query_sizes(q.cfg, q.rows, q.cols)
+    ts = q.tensor_scale if q.cfg.tensor_scale else None
+    for name, t, n in (("codes", q.codes, s.codes_bytes), ("scales", q.scales, s.n_scales), ("macro", q.macro, s.n_macro),
+                       ("offsets", q.offsets, 2 * s.n_offsets)):
+        if t is not None and (t.numel() * t.element_size() < n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be contiguous and hold {n} bytes")
+    if ts is not None and (ts.dtype != torch.float32 or ts.numel() < 1):
+        raise TypeError("tensor_scale must be float32")
+    for name, t in (("scales", q.scales), ("macro", q.macro), ("offsets", q.offsets), ("tensor_scale", ts)):
+        if t is not None and t.device != q.codes.device:
+            raise ValueError(f"{name} is on {t.device}, expected {q.codes.device}")
+
+
 def dequantize(q: Quantized, out_dtype: torch.dtype = torch.float32, stream=None,
                out: torch.Tensor | None = None) -> torch.Tensor:
     """x_hat from a ``Quantized`` (``mx_dequantize``); with a rotation the
     result is rotated back to the input space."""
     cfg = q.cfg
-    if out is None and stream is None and q.codes.is_cuda:
+    if out is None and stream is None:
         r = _binding().dequantize(q.codes, q.scales, q.tensor_scale, q.macro, q.offsets, cfg.address(), q.rows, q.cols, out_dtype)
         if r.__class__ is int:
             _check("mx_dequantize", r)
         return r
+    _check_held(q)
     if out is None:
         out = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.codes.device)
+    elif out.numel() < q.rows * q.cols or not out.is_contiguous():
+        raise ValueError(f"out must be contiguous and hold {q.rows} x {q.cols} elements")
+    if not q.codes.is_cuda:
+        raise ValueError("codes must be a CUDA tensor")
+    if out.device != q.codes.device:
+        raise ValueError(f"out is on {out.device}, expected {q.codes.device}")
     rc = mx_dequantize(cfg, _p(q.codes), _p(q.scales), _p(q.tensor_scale), _p(q.macro),
                        _p(q.offsets), q.rows, q.cols, _p(out), _dtype_code(out), _stream(stream))
     _check("mx_dequantize", rc)

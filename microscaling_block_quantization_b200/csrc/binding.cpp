@@ -342,14 +342,24 @@ PyObject *attn_decode(PyObject *const *a)
 // codes, scales, tensor_scale, macro, offsets, cfg address, rows, cols, out_dtype
 PyObject *dequantize(PyObject *const *a)
 {
-    const at::Tensor &codes = on_cuda(a[0], "codes"), &scales = tensor(a[1], "scales");
+    const at::Tensor &codes = tensor(a[0], "codes"), &scales = tensor(a[1], "scales");
     const at::Tensor *ts = maybe(a[2], "tensor_scale"), *macro = maybe(a[3], "macro"), *offsets = maybe(a[4], "offsets");
     const mx_config *cfg = address<mx_config>(a[5]);
     const int64_t rows = integer(a[6], "rows"), cols = integer(a[7], "cols");
     const at::ScalarType s = wanted(a[8], nullptr, at::kFloat);
+    mx_sizes n;
+    if (const int rc = mx_query_sizes(cfg, rows, cols, &n)) return PyLong_FromLong(rc);
+    if (cfg->tensor_scale == MX_TS_NONE) ts = nullptr;
+    buffer(&codes, n.codes_bytes, "codes");
+    buffer(&scales, n.n_scales, "scales");
+    buffer(macro, n.n_macro, "macro");
+    buffer(offsets, 2 * n.n_offsets, "offsets");
+    if (ts && (ts->scalar_type() != at::kFloat || ts->numel() < 1)) type_error("tensor_scale must be float32");
+    if (!codes.is_cuda()) value_error("codes must be a CUDA tensor");
     same_device(&scales, codes.device(), "scales");
     same_device(macro, codes.device(), "macro");
     same_device(offsets, codes.device(), "offsets");
+    same_device(ts, codes.device(), "tensor_scale");
     const int32_t od = dtype_code(s, "the result");
     const c10::Device dev = codes.device();
     const c10::cuda::CUDAGuard guard(dev);

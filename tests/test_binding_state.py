@@ -156,3 +156,58 @@ def test_a_cache_without_a_head_length_is_refused(mx, dim):
                                 lambda: mx.attn_decode(c, q, torch.zeros(1, 2, dtype=torch.int32), torch.zeros(1, dtype=torch.int32))]:
         with pytest.raises(ValueError, match="head_dim"):
             call()
+
+
+def quantized(mx, cfg, rows=128, cols=256):
+    import torch
+    s = mx.query_sizes(cfg, rows, cols)
+    z = lambda n, t=torch.uint8: torch.zeros(max(n, 1), dtype=t)  # noqa: E731
+    return mx.Quantized(cfg, rows, cols, z(s.codes_bytes), z(s.n_scales), torch.ones(1), z(s.n_macro) if cfg.macro_block else None,
+                        z(s.n_offsets, torch.int16) if cfg.asymmetric else None, None)
+
+
+def cut(name, by=1):
+    def change(q):
+        t = getattr(q, name)
+        setattr(q, name, t[:t.numel() - by])
+    return change
+
+
+def strided(name):
+    def change(q):
+        setattr(q, name, getattr(q, name).repeat_interleave(2)[::2])
+    return change
+
+
+@pytest.mark.parametrize("out", [False, True])
+@pytest.mark.parametrize("cfg,change,error,text", [
+    ({}, cut("codes"), ValueError, "codes must be contiguous and hold 16384"),
+    ({}, cut("scales"), ValueError, "scales must be contiguous and hold 1024"),
+    ({}, strided("codes"), ValueError, "codes must be contiguous"),
+    (dict(elem=2), lambda q: setattr(q, "codes", q.codes[:16384]), ValueError, "codes must be contiguous and hold 32768"),
+    (dict(axis=1), cut("scales"), ValueError, "scales must be contiguous and hold 1024"),
+    (dict(axis=2), cut("scales"), ValueError, "scales must be contiguous and hold 32"),
+    (dict(sf_layout=1), cut("scales"), ValueError, "scales must be contiguous and hold 1024"),
+    (dict(macro_block=128), cut("macro"), ValueError, "macro must be contiguous and hold 256"),
+    (dict(asymmetric=1), cut("offsets"), ValueError, "offsets must be contiguous and hold 2048"),
+    (dict(block=16, scale_fmt=1, rule=3, tensor_scale=1), cut("tensor_scale"), TypeError, "tensor_scale must be float32"),
+    (dict(block=16, scale_fmt=1, rule=3, tensor_scale=2), lambda q: setattr(q, "tensor_scale", q.tensor_scale.double()), TypeError,
+     "tensor_scale must be float32"),
+])
+def test_dequantize_checks_its_buffers(mx, cfg, change, error, text, out):
+    import torch
+    q = quantized(mx, mx.Config(**cfg))
+    more = dict(out=torch.zeros(128, 256)) if out else {}
+    with pytest.raises(ValueError, match="codes must be a CUDA tensor"):         # all that is wrong before the change
+        mx.dequantize(q, **more)
+    change(q)
+    with pytest.raises(error, match=text):
+        mx.dequantize(q, **more)
+
+
+def test_dequantize_checks_its_result(mx):
+    import torch
+    q = quantized(mx, mx.MXFP4)
+    for bad in (torch.zeros(128, 255), torch.zeros(256, 128).T, torch.zeros(128, 512)[:, ::2]):
+        with pytest.raises(ValueError, match="out must be contiguous"):
+            mx.dequantize(q, out=bad)
