@@ -126,6 +126,10 @@ void buffer(const at::Tensor *t, int64_t n, const char *name)
     if (t && ((int64_t)t->nbytes() < n || !t->is_contiguous()))
         value_error(std::string(name) + " must be contiguous and hold " + std::to_string(n) + " bytes");
 }
+void check_scale(const at::Tensor *t)
+{
+    if (t && (t->scalar_type() != at::kFloat || t->numel() < 1)) type_error("tensor_scale must be float32");
+}
 void *stream_of(c10::Device d) { return c10::cuda::getCurrentCUDAStream(d.index()).stream(); }
 
 // A cache as a call finds it: its tensors are looked at every time, so that none
@@ -180,8 +184,10 @@ void cache_on(const Cache &r, c10::Device dev)
 // x, codes, scales, tensor_scale, macro, offsets, cfg address, uses tensor scale, N, K, out_dtype, out
 PyObject *gemv(PyObject *const *a)
 {
+    const at::Tensor *ts = PyObject_IsTrue(a[7]) ? maybe(a[3], "tensor_scale") : nullptr;
+    check_scale(ts);
     const at::Tensor &x = on_cuda(a[0], "x"), &codes = tensor(a[1], "codes"), &scales = tensor(a[2], "scales");
-    const at::Tensor *ts = maybe(a[3], "tensor_scale"), *macro = maybe(a[4], "macro"), *offsets = maybe(a[5], "offsets");
+    const at::Tensor *macro = maybe(a[4], "macro"), *offsets = maybe(a[5], "offsets");
     const mx_config *cfg = address<mx_config>(a[6]);
     const int64_t N = integer(a[8], "N"), K = integer(a[9], "K");
     const at::Tensor *out = maybe(a[11], "out");
@@ -196,7 +202,6 @@ PyObject *gemv(PyObject *const *a)
     same_device(macro, dev, "macro");
     same_device(offsets, dev, "offsets");
     same_device(out, dev, "out");
-    if (!PyObject_IsTrue(a[7])) ts = nullptr;
     same_device(ts, dev, "tensor_scale");
     if (N >= 0 && K >= 0 && cfg->block > 0 && (K == 0 || N < (INT64_C(1) << 32) / K)) {
         const int64_t blocks = N * (K / cfg->block);
@@ -204,7 +209,6 @@ PyObject *gemv(PyObject *const *a)
         buffer(&scales, blocks, "scales");
         buffer(macro, cfg->macro_block ? N * (K / 128) : 0, "macro");
         buffer(offsets, cfg->asymmetric ? 2 * blocks : 0, "offsets");
-        buffer(ts, 4, "tensor_scale");
     }
     const at::ScalarType ys = wanted(a[10], out, x.scalar_type());
     const int32_t yd = dtype_code(ys, "the result");
@@ -354,7 +358,7 @@ PyObject *dequantize(PyObject *const *a)
     buffer(&scales, n.n_scales, "scales");
     buffer(macro, n.n_macro, "macro");
     buffer(offsets, 2 * n.n_offsets, "offsets");
-    if (ts && (ts->scalar_type() != at::kFloat || ts->numel() < 1)) type_error("tensor_scale must be float32");
+    check_scale(ts);
     if (!codes.is_cuda()) value_error("codes must be a CUDA tensor");
     same_device(&scales, codes.device(), "scales");
     same_device(macro, codes.device(), "macro");

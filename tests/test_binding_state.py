@@ -211,3 +211,14 @@ def test_dequantize_checks_its_result(mx):
     for bad in (torch.zeros(128, 255), torch.zeros(256, 128).T, torch.zeros(128, 512)[:, ::2]):
         with pytest.raises(ValueError, match="out must be contiguous"):
             mx.dequantize(q, out=bad)
+
+
+def test_gemv_checks_its_tensor_scale(mx):
+    import torch
+    q = quantized(mx, given(mx), 64, 256)
+    for change in (lambda: setattr(q, "tensor_scale", q.tensor_scale.double()), lambda: setattr(q, "tensor_scale", torch.ones(0))):
+        with pytest.raises(ValueError, match="CUDA"):
+            mx.gemv(torch.zeros(1, 256), quantized(mx, given(mx), 64, 256))
+        change()
+        with pytest.raises(TypeError, match="tensor_scale must be float32"):
+            mx.gemv(torch.zeros(1, 256), q)
