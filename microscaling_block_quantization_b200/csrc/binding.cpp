@@ -181,6 +181,22 @@ void cache_on(const Cache &r, c10::Device dev)
     for (const at::Tensor *t : r.all) same_device(t, dev, "the cache");
 }
 
+// Other Python threads run while a call launches, which waits
+// while the launch queue is full.
+class Unlocked {
+    PyThreadState *state = PyEval_SaveThread();
+
+public:
+    Unlocked() = default;
+    Unlocked(const Unlocked &) = delete;
+    ~Unlocked() { PyEval_RestoreThread(state); }
+};
+template <typename F> auto unlocked(F f)
+{
+    const Unlocked here;
+    return f();
+}
+
 // x, codes, scales, tensor_scale, macro, offsets, cfg address, uses tensor scale, N, K, out_dtype, out
 PyObject *gemv(PyObject *const *a)
 {
@@ -223,9 +239,11 @@ PyObject *gemv(PyObject *const *a)
     } else {
         y = vec ? at::empty({N}, x.options().dtype(ys)) : at::empty({M, N}, x.options().dtype(ys));
     }
-    const int rc = mx_gemv(cfg, x.data_ptr(), xd, ldx, M, codes.data_ptr(), static_cast<uint8_t *>(scales.data_ptr()),
-                           static_cast<float *>(ptr(ts)), static_cast<uint8_t *>(ptr(macro)), static_cast<uint16_t *>(ptr(offsets)),
-                           N, K, y.data_ptr(), yd, ldy, stream_of(dev));
+    const int rc = unlocked([&] {
+        return mx_gemv(cfg, x.data_ptr(), xd, ldx, M, codes.data_ptr(), static_cast<uint8_t *>(scales.data_ptr()),
+                       static_cast<float *>(ptr(ts)), static_cast<uint8_t *>(ptr(macro)), static_cast<uint16_t *>(ptr(offsets)),
+                       N, K, y.data_ptr(), yd, ldy, stream_of(dev));
+    });
     return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(y));
 }
 
@@ -261,6 +279,7 @@ PyObject *kv_append(PyObject *const *a)
     void *pq = vector(q_gain, D, at::kFloat, dev, "q_gain"), *pk = vector(k_gain, D, at::kFloat, dev, "k_gain");
     void *pl = vector(&slots, T, at::kLong, dev, "slots");
     const float eps = real(a[7], "eps");
+    const int32_t interleaved = PyObject_IsTrue(a[9]) ? 1 : 0;
     const c10::cuda::CUDAGuard guard(dev);
     int64_t ldqo = Hq * D, ldko = H * D;
     at::Tensor qo, ko;
@@ -276,10 +295,12 @@ PyObject *kv_append(PyObject *const *a)
     } else if (make_k) {
         ko = at::empty({T, H, D}, k.options());
     }
-    const int rc = mx_kv_append(cfg, &cache.c, ptr(q), k.data_ptr(), v.data_ptr(), dt, ldq, ldk, ldv, T, (int32_t)Hq,
-                                static_cast<float *>(pq), static_cast<float *>(pk), eps, static_cast<float *>(pf), (int32_t)rot,
-                                PyObject_IsTrue(a[9]) ? 1 : 0, static_cast<int64_t *>(ps), static_cast<int64_t *>(pl),
-                                qo.defined() ? qo.data_ptr() : nullptr, ldqo, ko.defined() ? ko.data_ptr() : nullptr, ldko, stream_of(dev));
+    const int rc = unlocked([&] {
+        return mx_kv_append(cfg, &cache.c, ptr(q), k.data_ptr(), v.data_ptr(), dt, ldq, ldk, ldv, T, (int32_t)Hq,
+                            static_cast<float *>(pq), static_cast<float *>(pk), eps, static_cast<float *>(pf), (int32_t)rot,
+                            interleaved, static_cast<int64_t *>(ps), static_cast<int64_t *>(pl),
+                            qo.defined() ? qo.data_ptr() : nullptr, ldqo, ko.defined() ? ko.data_ptr() : nullptr, ldko, stream_of(dev));
+    });
     if (rc) return PyLong_FromLong(rc);
     PyObject *r = PyTuple_New(2);
     if (!r) return nullptr;
@@ -330,10 +351,12 @@ PyObject *attn_decode(PyObject *const *a)
     const int64_t nbytes = mx_attn_workspace_bytes(&cache.c, S, (int32_t)Hq, pages, (int32_t)window, (int32_t)sinks);
     if (given) ws = *given;
     else if (nbytes) ws = at::empty({nbytes}, q.options().dtype(at::kByte));
-    const int rc = mx_attn_decode(cfg, &cache.c, q.data_ptr(), qd, ldq, S, (int32_t)Hq, static_cast<int32_t *>(table.data_ptr()), ldt, pages,
-                                  static_cast<int32_t *>(pl), scale, (int32_t)window, (int32_t)sinks, o.data_ptr(), od, ldo,
-                                  want_lse ? static_cast<float *>(l.data_ptr()) : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
-                                  ws.defined() ? ws.numel() : 0, stream_of(dev));
+    const int rc = unlocked([&] {
+        return mx_attn_decode(cfg, &cache.c, q.data_ptr(), qd, ldq, S, (int32_t)Hq, static_cast<int32_t *>(table.data_ptr()), ldt, pages,
+                              static_cast<int32_t *>(pl), scale, (int32_t)window, (int32_t)sinks, o.data_ptr(), od, ldo,
+                              want_lse ? static_cast<float *>(l.data_ptr()) : nullptr, ws.defined() ? ws.data_ptr() : nullptr,
+                              ws.defined() ? ws.numel() : 0, stream_of(dev));
+    });
     if (rc) return PyLong_FromLong(rc);
     if (!want_lse) return THPVariable_Wrap(std::move(o));
     PyObject *r = PyTuple_New(2);
@@ -368,9 +391,11 @@ PyObject *dequantize(PyObject *const *a)
     const c10::Device dev = codes.device();
     const c10::cuda::CUDAGuard guard(dev);
     at::Tensor out = at::empty({rows, cols}, codes.options().dtype(s));
-    const int rc = mx_dequantize(cfg, codes.data_ptr(), static_cast<uint8_t *>(scales.data_ptr()), static_cast<float *>(ptr(ts)),
-                                 static_cast<uint8_t *>(ptr(macro)), static_cast<uint16_t *>(ptr(offsets)), rows, cols, out.data_ptr(),
-                                 od, stream_of(dev));
+    const int rc = unlocked([&] {
+        return mx_dequantize(cfg, codes.data_ptr(), static_cast<uint8_t *>(scales.data_ptr()), static_cast<float *>(ptr(ts)),
+                             static_cast<uint8_t *>(ptr(macro)), static_cast<uint16_t *>(ptr(offsets)), rows, cols, out.data_ptr(),
+                             od, stream_of(dev));
+    });
     return rc ? PyLong_FromLong(rc) : THPVariable_Wrap(std::move(out));
 }
 

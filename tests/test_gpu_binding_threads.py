@@ -1,0 +1,52 @@
+"""Other Python threads run while a call of the compiled binding waits for room
+in a full launch queue."""
+import threading
+import time
+
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def mx():
+    from microscaling_block_quantization_b200 import build
+    build.build()
+    import microscaling_block_quantization_b200 as m
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return m
+
+
+@pytest.mark.parametrize("name", ["gemv", "dequantize", "kv_append", "attn_decode"])
+def test_threads_run_beside_a_call_that_waits(mx, name):
+    w = mx.quantize(torch.randn(64, 256, device="cuda").bfloat16(), stats=False)
+    x = torch.randn(1, 256, device="cuda").bfloat16()
+    c = mx.kv_cache(2, 16, 1, 64)
+    heads, slots = x.view(4, 64), torch.arange(4, device="cuda")
+    table, n = torch.tensor([[0, 1]], dtype=torch.int32, device="cuda"), torch.tensor([4], dtype=torch.int32, device="cuda")
+    call = {"gemv": lambda: mx.gemv(x, w), "dequantize": lambda: mx.dequantize(w), "kv_append": lambda: mx.kv_append(c, None, heads, heads, slots),
+            "attn_decode": lambda: mx.attn_decode(c, heads[:1], table, n)}[name]
+    call()
+    torch.cuda.synchronize()
+    longest = []
+
+    def work():
+        for _ in range(4000):                                # more than a launch queue holds
+            t = time.perf_counter()
+            call()
+            longest.append(time.perf_counter() - t)
+
+    torch.cuda._sleep(1_000_000_000)                         # half a second of device time
+    worker = threading.Thread(target=work)
+    worker.start()
+    gap, last = 0.0, time.perf_counter()
+    while worker.is_alive():
+        time.sleep(0.001)
+        now = time.perf_counter()
+        gap, last = max(gap, now - last), now
+    worker.join()
+    torch.cuda.synchronize()
+    # the call that waited longest held this thread up for a fraction of its time
+    assert gap < max(0.1, 0.5 * max(longest)), (gap, max(longest))
