@@ -26,7 +26,6 @@ from . import inputs  # noqa: F401  (seeded synthetic workloads)
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_lib", "libmx_b200.so")
-BINDING_PATH = os.path.join(_HERE, "_lib", "mx_binding.so")
 
 # ---- constants of include/mx.h ------------------------------------------
 MX_OK = 0
@@ -189,15 +188,20 @@ def lib() -> C.CDLL:
 _compiled = None
 
 
-def _binding():
-    """The compiled marshalling of the decode-time operators."""
+def _binding(needed: bool = True):
+    """The compiled marshalling of the decode-time operators (None where it is
+    not needed and was not built for this Python and torch)."""
     global _compiled
     if _compiled is None:
+        from .build import binding_path
         lib()
-        if not os.path.exists(BINDING_PATH):
-            raise RuntimeError(f"{BINDING_PATH} is missing: build it with "
+        path = binding_path()
+        if not os.path.exists(path):
+            if not needed:
+                return None
+            raise RuntimeError(f"{path} is missing: build it with "
                                "`python -c 'import __graft_entry__ as g; g.build()'`")
-        spec = importlib.util.spec_from_file_location("mx_binding", BINDING_PATH)
+        spec = importlib.util.spec_from_file_location("mx_binding", path)
         m = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(m)
         _compiled = m
@@ -527,8 +531,9 @@ def dequantize(q: Quantized, out_dtype: torch.dtype = torch.float32, stream=None
     """x_hat from a ``Quantized`` (``mx_dequantize``); with a rotation the
     result is rotated back to the input space."""
     cfg = q.cfg
-    if out is None and stream is None:
-        r = _binding().dequantize(q.codes, q.scales, q.tensor_scale, q.macro, q.offsets, cfg.address(), q.rows, q.cols, out_dtype)
+    b = _binding(needed=False) if out is None and stream is None else None
+    if b is not None:
+        r = b.dequantize(q.codes, q.scales, q.tensor_scale, q.macro, q.offsets, cfg.address(), q.rows, q.cols, out_dtype)
         if r.__class__ is int:
             _check("mx_dequantize", r)
         return r
@@ -541,6 +546,9 @@ def dequantize(q: Quantized, out_dtype: torch.dtype = torch.float32, stream=None
         raise ValueError("codes must be a CUDA tensor")
     if out.device != q.codes.device:
         raise ValueError(f"out is on {out.device}, expected {q.codes.device}")
+    if stream is None and q.codes.device.index != torch.cuda.current_device():
+        with torch.cuda.device(q.codes.device):
+            return dequantize(q, out_dtype, None, out)
     rc = mx_dequantize(cfg, _p(q.codes), _p(q.scales), _p(q.tensor_scale), _p(q.macro),
                        _p(q.offsets), q.rows, q.cols, _p(out), _dtype_code(out), _stream(stream))
     _check("mx_dequantize", rc)

@@ -24,7 +24,6 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 OBJ_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmx_b200.so")
-BINDING = os.path.join(OUT_DIR, "mx_binding.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -49,10 +48,17 @@ def _deps() -> list[str]:
     return deps
 
 
+def binding_path() -> str:
+    """The compiled binding for this Python and this torch: it holds the ABI of both."""
+    import torch
+    return os.path.join(OUT_DIR, f"mx_binding.torch-{torch.__version__}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+    binding = binding_path()
+    if not os.path.exists(LIB) or not os.path.exists(binding):
         return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    t = min(os.path.getmtime(LIB), os.path.getmtime(binding))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -87,13 +93,13 @@ def _compile_binding() -> str:
 def _link_binding(obj: str) -> None:
     import torch
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
-    tmp = BINDING + ".tmp"
+    tmp = binding_path() + ".tmp"
     cmd = ["g++", "-shared", obj, "-o", tmp, "-L", OUT_DIR, "-l:libmx_b200.so", "-L", lib, "-lc10", "-lc10_cuda", "-ltorch_cpu",
            "-ltorch_python", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, BINDING)
+    os.replace(tmp, binding_path())
 
 
 def build(force: bool = False, verbose: bool = False) -> str:

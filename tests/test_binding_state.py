@@ -222,3 +222,28 @@ def test_gemv_checks_its_tensor_scale(mx):
         change()
         with pytest.raises(TypeError, match="tensor_scale must be float32"):
             mx.gemv(torch.zeros(1, 256), q)
+
+
+def test_a_binding_built_for_another_torch_is_not_loaded(mx, monkeypatch):
+    import sysconfig
+
+    import torch
+    from microscaling_block_quantization_b200 import build
+    assert build.up_to_date()
+    mine = build.binding_path()
+    assert torch.__version__ in mine and mine.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(mx, "_compiled", None)
+    assert mx._binding().__file__ == mine
+    monkeypatch.setattr(mx, "_compiled", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    assert not build.up_to_date()
+    with pytest.raises(RuntimeError, match="missing"):
+        mx.gemv(torch.zeros(1, 256), quantized(mx, mx.MXFP4))
+
+
+def test_dequantize_needs_no_binding(mx, monkeypatch):
+    import torch
+    monkeypatch.setattr(mx, "_compiled", None)
+    monkeypatch.setattr(torch, "__version__", "0.0.1")
+    with pytest.raises(ValueError, match="codes must be a CUDA tensor"):
+        mx.dequantize(quantized(mx, mx.MXFP4))

@@ -43,3 +43,15 @@ def test_replaced_buffers(mx):
     tol = want.abs() * 2.0 ** -8 + torch.einsum("hl,lhd->hd", p, vh.abs()) * 2.0 ** -11
     assert bool(((again[0].double() - want).abs() <= tol).all())
     assert torch.equal(first, again)                         # scales twice as large, scale codes half: the same values
+
+
+def test_dequantize_without_the_compiled_binding(mx, monkeypatch):
+    for cfg in (mx.MXFP4, mx.NVFP4, mx.Config(elem=mx.E2M3), mx.Config(axis=mx.AXIS_COL)):
+        q = mx.quantize(torch.randn(64, 256, device="cuda").bfloat16(), cfg, stats=False)
+        for dtype in (torch.float32, torch.bfloat16):
+            want = mx.dequantize(q, dtype)
+            with monkeypatch.context() as m:
+                m.setattr(mx, "_compiled", None)
+                m.setattr(torch, "__version__", "0.0.1")
+                got = mx.dequantize(q, dtype)
+            assert torch.equal(got, want)
