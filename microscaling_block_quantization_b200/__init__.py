@@ -595,6 +595,15 @@ def gemm(qa: Quantized, qb: Quantized, out_dtype: torch.dtype = torch.bfloat16,
 
 
 # ---- decode-time operators --------------------------------------------------
+def _on(stream, tensor):
+    """The stream's context; its device must be the tensors', whose current
+    stream would be used instead."""
+    device = getattr(tensor, "device", stream.device)        # (the binding refuses what is no tensor)
+    if stream.device != device:
+        raise ValueError(f"the stream is on {stream.device}, expected {device}")
+    return torch.cuda.stream(stream)
+
+
 def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *,
          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """y = x W^T of a few rows x (``[M, K]`` or ``[K]``, bf16 or fp32, rows at
@@ -604,7 +613,7 @@ def gemv(x: torch.Tensor, qw: Quantized, out_dtype: torch.dtype | None = None, *
     On a ``stream`` of the caller's the result is allocated there; x and qw must
     be ready on it."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, x):
             return gemv(x, qw, out_dtype, out=out)
     cfg = qw.cfg
     r = _binding().gemv(x, qw.codes, qw.scales, qw.tensor_scale, qw.macro, qw.offsets, cfg.address(), cfg.tensor_scale, qw.rows,
@@ -686,7 +695,7 @@ def kv_append(cache: KVCache, q: torch.Tensor | None, k: torch.Tensor, v: torch.
     ``[T, q_heads, head_dim]`` (into ``q_out`` when given; it may be q) and, when ``k_out`` is
     True or a tensor, the rotated keys, else None."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, k):
             return kv_append(cache, q, k, v, slots, positions, q_gain=q_gain, k_gain=k_gain, eps=eps, inv_freq=inv_freq,
                              interleaved=interleaved, q_out=q_out, k_out=k_out)
     r = _binding().kv_append(*cache._parts(), q, k, v, slots, positions, q_gain, k_gain, eps, inv_freq, interleaved, q_out, k_out)
@@ -707,7 +716,7 @@ def attn_decode(cache: KVCache, q: torch.Tensor, page_table: torch.Tensor, lengt
     ``out_dtype`` or ``out`` says otherwise, and with ``lse`` also the log sum exp, fp32
     ``[S, q_heads]``.  Scratch is allocated per call unless ``workspace`` (uint8) is given."""
     if stream is not None:
-        with torch.cuda.stream(stream):
+        with _on(stream, q):
             return attn_decode(cache, q, page_table, lengths, scale=scale, window=window, sinks=sinks, lse=lse,
                                out_dtype=out_dtype, out=out, workspace=workspace)
     r = _binding().attn_decode(*cache._parts(), q, page_table, lengths, max(cache.head_dim, 1) ** -0.5 if scale is None else scale, window,

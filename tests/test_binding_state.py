@@ -247,3 +247,16 @@ def test_dequantize_needs_no_binding(mx, monkeypatch):
     monkeypatch.setattr(torch, "__version__", "0.0.1")
     with pytest.raises(ValueError, match="codes must be a CUDA tensor"):
         mx.dequantize(quantized(mx, mx.MXFP4))
+
+
+def test_a_stream_of_another_device_is_refused(mx):
+    import types
+
+    import torch
+    stream = types.SimpleNamespace(device=torch.device("cuda", 1), cuda_stream=0)
+    zeros, c = torch.zeros, small_cache(mx)
+    for call in (lambda: mx.gemv(zeros(1, 256), quantized(mx, mx.MXFP4), stream=stream),
+                 lambda: mx.kv_append(c, None, zeros(1, 64), zeros(1, 64), zeros(1, dtype=torch.int64), stream=stream),
+                 lambda: mx.attn_decode(c, zeros(1, 1, 64), zeros(1, 2, dtype=torch.int32), zeros(1, dtype=torch.int32), stream=stream)):
+        with pytest.raises(ValueError, match="the stream is on cuda:1, expected cpu"):
+            call()
