@@ -432,7 +432,8 @@ int mx_mbs_gemm_scales(const mx_config *cfg, const uint8_t *scales, const uint8_
  *                == MX_TS_NONE.
  *   y            device, bf16 or fp32 (y_dtype), row m at y + m ldy elements
  *                (ldy >= N); must not overlap an input.
- * Products q x are exact and summed in binary32, one sum per block times its
+ * Products q x are exact (binary32 x is taken to 2^-23 of each value: one in
+ * four loses its last bit) and summed in binary32, one sum per block times its
  * scale; every output is rounded once, and its value does not depend on
  * timing.  A chunk's sums are formed with its x scaled to 2^14 .. 2^15, and
  * pass binary32 where weights pass about 2^100.  x values of a 128-column chunk below 2^-31 of the chunk's largest
@@ -517,7 +518,8 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
  *                sequence without a visible token gives zeros and -inf.
  *   workspace    mx_attn_workspace_bytes() bytes, 16-byte aligned, not
  *                initialised; calls that may run at the same time need their own.
- * Scores, softmax statistics and sums are binary32; the weights are rounded to
+ * Scores (of binary32 queries to 2^-23 of each value), softmax statistics and
+ * sums are binary32; the weights are rounded to
  * 11 bits for bf16 results and to 22 when q or out is fp32.  A token's part of
  * a 32-element block of the head is dropped only where its weight times the
  * block's scale is below 2^-24 of the largest weight times the smallest scale there

@@ -16,7 +16,7 @@
 //
 // * Scores: 16 tokens x 8 heads, codes as the 16-row operand, queries as f16
 //   pieces scaled by a power of two per head (bf16: one piece exact down to
-//   2^-31 of the head's largest; binary32: two, exact); each block's sum times
+//   2^-31 of the head's largest; binary32: two, to 2^-23); each block's sum times
 //   its scale in binary32.
 // * One pass with a running maximum m (reference for the exponentials) and
 //   sum l per head in binary32.  m moves only when a score exceeds it by 4

@@ -14,9 +14,11 @@
 // * x as f16 pieces.  Products of codes and f16 values are exact in the
 //   matrix instruction and summed in binary32.  Each 128-column chunk of a
 //   token is scaled by a power of two to [2^14, 2^15): a bf16 value down to
-//   2^-31 of its chunk's largest is one f16 exactly; a binary32 value is the
-//   sum of two (11 + 12 bits) exactly, the second scaled by 2^11.  Smaller
-//   values are rounded at 2^-39 (bf16) or 2^-50 of the chunk's largest.
+//   2^-31 of its chunk's largest is one f16 exactly; a binary32 value is two,
+//   the second scaled by 2^11: of the at most 12 bits that the first leaves it
+//   holds 11, so a quarter of values lose their last bit, 2^-23 at most (a third
+//   piece would be half as many matrix instructions again).  Smaller values are
+//   rounded at 2^-39 (bf16) or 2^-50 of the chunk's largest.
 // * Work is split into units of 16 rows x 256 columns (128 where K is no
 //   multiple of 256).  A cluster of C CTAs splits K (each CTA keeps its slice of x in shared memory), its CTAs' 16
 //   warps split rows and, KS ways, the slice.  Each warp streams its units
@@ -326,7 +328,7 @@ __device__ void gv_stage_x(const GvParams &p, const GvGeom &gm, uint8_t *smem, i
                 const __half2 hh = __floats2half2_rn(a, b);
                 h[0][i] = *reinterpret_cast<const uint32_t *>(&hh);
                 if (FP32) {
-                    // what the first piece leaves, exact; an infinite or NaN
+                    // what the first piece leaves (12 bits at most); an infinite or NaN
                     // value is all in the first piece
                     const float2 back = __half22float2(hh);
                     float ra = __fmul_rn(__fsub_rn(a, back.x), 2048.0f), rb = __fmul_rn(__fsub_rn(b, back.y), 2048.0f);
