@@ -438,7 +438,9 @@ int mx_mbs_gemm_scales(const mx_config *cfg, const uint8_t *scales, const uint8_
  * timing.  A chunk's sums are formed with its x scaled to 2^14 .. 2^15, and
  * pass binary32 where weights pass about 2^100.  x values of a 128-column chunk below 2^-31 of the chunk's largest
  * are rounded at 2^-39 of it (binary32 x: at 2^-50).  An infinite or NaN x
- * gives what IEEE sums of the products give; a NaN scale a NaN.
+ * gives what IEEE sums of the products give (with offsets, whose parts o sum x are
+ * summed apart from q x: an infinity or a NaN, whatever the weights' signs); a NaN
+ * scale a NaN.
  * 0 <= M <= 2^17; the weights are read once per 16 rows of bf16 x (8 of
  * fp32).  No workspace; one launch.
  */

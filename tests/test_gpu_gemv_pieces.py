@@ -37,3 +37,17 @@ def test_one_value_of_every_significand(mx, K, dtype):
     want = value.double()[:, None] * wd.T[at]
     lost = 0.0 if dtype == torch.bfloat16 else 2.0 ** -23 + 2.0 ** -24 * (1 + 2.0 ** -23)
     assert bool(((y - want).abs() <= lost * want.abs()).all())
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("cfg", [dict(asymmetric=1, elem=4, rule=1), dict(asymmetric=1, elem=4, rule=1, block=128), dict(asymmetric=1)])
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_not_finite_x_with_offsets(mx, bad, cfg, dtype):
+    """(q s) x and o x are summed apart: an infinite x gives infinities or NaN, in its own token alone."""
+    w = mx.quantize(inputs.normal(96, 512, 0.02, 3).cuda(), mx.Config(**cfg), stats=False)
+    x = inputs.small_normal(3, 512, 1).cuda().to(dtype)
+    fine = mx.gemv(x, w)
+    x[1, 300] = bad
+    y = mx.gemv(x, w)
+    assert not bool(torch.isfinite(y[1]).any())
+    assert torch.equal(y[0], fine[0]) and torch.equal(y[2], fine[2]) and bool(torch.isfinite(fine).all())
