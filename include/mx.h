@@ -511,6 +511,7 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
  *   page_table   device, int32: entry j of row s (at s ld_table + j, j < max_pages)
  *                is the page of the sequence's tokens [j page_size, (j + 1) page_size).
  *                The tokens of an entry outside [0, pages) are not visible.
+ *                max_pages page_size < 2^31 - 64.
  *   lengths      device, int32: the sequence's tokens, the query's own included
  *                (clamped to [0, max_pages page_size]).
  *   window       0: every token is visible.  Else the last `window` tokens and

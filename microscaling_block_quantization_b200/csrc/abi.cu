@@ -594,7 +594,8 @@ int mx_attn_decode(const mx_config *cfg, const mx_kv_cache *cache, const void *q
     if ((q_dtype != MX_DT_BF16 && q_dtype != MX_DT_FP32) || (out_dtype != MX_DT_BF16 && out_dtype != MX_DT_FP32))
         return MX_ERR_INVALID;
     if (seqs < 0 || seqs > (1 << 20) || q_heads < 1 || q_heads > 65536 || q_heads % cache->kv_heads) return MX_ERR_INVALID;
-    if (max_pages < 0 || max_pages > INT32_MAX || max_pages * cache->page_size > INT32_MAX || window < 0 || sinks < 0)
+    // (a tile's lanes number tokens past the last one)
+    if (max_pages < 0 || max_pages > INT32_MAX || max_pages * cache->page_size > INT32_MAX - 64 || window < 0 || sinks < 0)
         return MX_ERR_INVALID;
     if (!(scale > -INFINITY && scale < INFINITY)) return MX_ERR_INVALID;
     if (seqs * q_heads > INT32_MAX) return MX_ERR_INVALID;   // the launch grids
