@@ -491,7 +491,8 @@ typedef struct {
  *                a slot outside the cache (-1 for padding) stores nothing.  Slots of
  *                one call must differ: two tokens with one slot leave a mixture.
  *   q_out        device, dtype; may be q itself (same ld).  k_out: the rotated
- *                keys in dtype, or NULL; may be k itself.
+ *                keys in dtype, or NULL; may be k itself.  Outputs overlap nothing
+ *                else (v apart from k too, where k_out is k).
  * One launch, no workspace; rows that no slot names stay as they were.
  */
 int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, const void *k, const void *v,

@@ -84,12 +84,12 @@ AtPick at_pick(int el, int d, int bs, int nth, int hp, int sfmt)
 }  // namespace
 
 // How a call of these sizes is split (times on a B200, both sides measured with one
-// kernel, a tenth slower than now; 32 query and 8 key heads of 128, MXFP4 unless said).  As many stretches of 32 tokens at least as run at
+// kernel, 157 us for the first of these sizes, and not again; 32 query and 8 key heads of 128, MXFP4 unless said).  As many stretches of 32 tokens at least as run at
 // once (`warps_sm` warps of the kernel an SM); where several long sequences give
 // stretches of 256 tokens and more, twice as many, so that a warp that is done
 // makes room for another: 64 sequences of up to 8192 tokens 176 -> 156 us, but
 // 256 of up to 300 33 -> 39 us.
-// A second launch that joins the stretches costs 3 to 5 us.  Where there are
+// A second launch costs 2.5 us empty, and 3 to 5 with the join in it.  Where there are
 // CTAs for half the SMs and more, a CTA's warps are a sequence's stretches and
 // join them: 16 x 1000 15.3 -> 12.4 us, NVFP4 64 x 1000 42 -> 37 us, 128 x 2048 92 -> 85
 // us.  With fewer CTAs, warps that share few SMs lose more than the launch costs

@@ -44,19 +44,20 @@
 //   products p v are formed with w as TF32, the same 11 bits (binary32: two
 //   pieces) with binary32's exponents, four m16n8k8 instructions for two, and
 //   nothing is dropped, in a loop of its own: as a branch of the one loop it cost
-//   every call 5% (64 x 8192 134 -> 140 us, this way 136).  So w is dropped only
-//   below 2^-24 of the largest weight times the block's smallest scale (2^-26 but at
-//   the top of UE5M3).  VM = 1, whose weights are p alone, drops p below 2^-35 of
-//   the largest.
+//   every call 5% (64 x 8192 134 -> 140 us, this way 136; with every stretch wide
+//   316 us).  So w is dropped only below 2^-24 of the largest weight times the
+//   block's smallest scale (2^-26 but at the top of UE5M3).  VM = 1, whose weights
+//   are p alone, drops p below 2^-35 of the largest.
 // * Partial results (each stretch's own attention, m, l) of a sequence's
 //   stretches meet in a fixed order: where a CTA's warps hold them all, in
 //   shared memory at the end of the kernel, else in a second launch.
 //
 // Measured (32 query heads, 8 key heads of 128): 64 sequences of up to 8192
-// tokens in MXFP4 132 us (3.3 TB/s), one of 131072 in NVFP4 57 us: the integer
-// and conversion pipe is 55% and the issue slots 61% taken (360 instructions for
-// 16 tokens of a key head).  One sequence of 1000 tokens 8.7 us: two launches,
-// and 0.6 us for each 16 tokens of a warp.
+// tokens in MXFP4 134 us (3.2 TB/s), one of 131072 in NVFP4 56 us: the integer
+// and conversion pipe is 57% and the issue slots 64% taken (378 instructions for
+// 16 tokens of a key head), with four warps a scheduler to hide what each waits
+// for.  One sequence of 1000 tokens 8.9 us: two launches, and 0.6 us for each
+// 16 tokens of a warp.
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -30,7 +30,9 @@ __device__ __forceinline__ uint32_t hadd2_u(uint32_t a, uint32_t b)
 }
 
 // Eight codes of a word -> four f16x2 of their grid values, codes (2i, 2i+1)
-// in h[i].  E2M1: the conversion instruction.  INT4: a byte's nibbles spread
+// in h[i].  E2M1: the conversion instruction.  INT4 (integers under an f16
+// exponent, Kim, Henry, Fahim and Hassan Awadalla, "Who Says Elephants Can't Run",
+// 2022): a byte's nibbles spread
 // to the two halves (multiply by 2^12 + 1, mask) under the exponent of 1024,
 // where an f16 ulp is 1, then 1024 (+ 8 for two's complement, whose sign bit
 // is flipped first) taken off: exact.  E3M0: the 3-bit magnitude is an f16
