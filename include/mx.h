@@ -526,10 +526,10 @@ int mx_kv_append(const mx_config *cfg, const mx_kv_cache *cache, const void *q, 
  * sums are binary32; the weights are rounded to
  * 11 bits for bf16 results and to 22 when q or out is fp32.  A token's part of
  * a 32-element block of the head is dropped only where its weight times the
- * block's scale is below 2^-24 of the largest weight times the smallest scale there
- * (scale code 0 aside); E2M1 with UE4M3 scales in blocks of 16 or 32: where its weight is
- * below 2^-35 of the largest.  Values may reach
- * the ends of binary32; a score's sum is formed with the head's queries scaled
+ * block's scale is below 2^-24 of the largest weight times the block's smallest
+ * scale (scale code 0 aside) in the stretch of the sequence that one warp takes;
+ * E2M1 with UE4M3 scales in blocks of 16 or 32: where its weight is below 2^-35 of the
+ * stretch's largest.  Values may reach the ends of binary32; a score's sum is formed with the head's queries scaled
  * to 2^14 .. 2^15, and passes binary32 where keys pass about 2^100.  One launch,
  * two where sequences are split over several CTAs; the split goes by the sizes
  * given on the host, so results do not depend on timing.
