@@ -48,5 +48,5 @@ def test_threads_run_beside_a_call_that_waits(mx, name):
         gap, last = max(gap, now - last), now
     worker.join()
     torch.cuda.synchronize()
-    # the call that waited longest held this thread up for a fraction of its time
-    assert gap < max(0.1, 0.5 * max(longest)), (gap, max(longest))
+    # this thread was held up for less than half of the wait (0.5 s, where a call holds the lock)
+    assert gap < 0.25, (gap, max(longest))
